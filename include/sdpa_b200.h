@@ -70,9 +70,12 @@ typedef enum {
   ATTN_ERR_SCALE = 11,         /* scale is negative, NaN or infinite */
   ATTN_ERR_SCRATCH_LIMIT = 12, /* attn_decode_splitkv_static: problem needs more than
                                   ATTN_STATIC_SCRATCH_BYTES of scratch */
-  ATTN_ERR_SEQLEN = 13         /* reported by attn_check_device_error: a per-batch length read on
+  ATTN_ERR_SEQLEN = 13,        /* reported by attn_check_device_error: a per-batch length read on
                                   the device was outside its valid range and was clamped, or a
                                   position of attn_rope_append was out of range and skipped */
+  ATTN_ERR_PAGE = 14           /* a page size or page stride the paged entry points lack; reported by
+                                  attn_check_device_error: a page id or slot was out of range, or
+                                  attn_page_plan refused a request */
 } attn_status_t;
 
 enum { ATTN_CAUSAL_NONE = 0, ATTN_CAUSAL_TOP_LEFT = 1, ATTN_CAUSAL_BOTTOM_RIGHT = 2 };
@@ -343,6 +346,119 @@ attn_status_t attn_rope_append(const void* packed_qkv, const float* cos_table, c
                                int B, int S_new, int Hq, int Hkv, int cap, int d, int layout, void* stream);
 
 /*
+ * A paged KV cache.  K and V are two pools of pages of page_size rows (page_size
+ * a power of two, 16 to 256), laid out
+ *   ATTN_LAYOUT_BHSD  [num_pages, Hkv, page_size, d] bf16
+ *   ATTN_LAYOUT_BSHD  [num_pages, page_size, Hkv, d] bf16
+ * dense inside a page; page_stride is the distance between two pages in
+ * elements (0 = dense: Hkv * page_size * d; else a multiple of 8, at least
+ * that), the same for both pools, so K and V pages may alternate in one
+ * allocation.  Slot s is row s mod page_size of page s / page_size;
+ * num_pages * page_size must not exceed 2^31.
+ *   block_table  device int32 [B, max_pages]: key j of sequence b is in row
+ *                j mod page_size of page block_table[b][j / page_size].  Only
+ *                the entries of keys that a call reads are looked at.  Two
+ *                sequences may share pages that neither appends to.
+ * The table, the lengths and the slots below are read by the kernels only, so
+ * earlier work on `stream` may write them.
+ */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  const int* block_table;  /* unused by attn_rope_append_paged */
+  long long page_stride;
+  int num_pages;
+  int page_size;
+  int max_pages;           /* entries per row of block_table; unused by attn_rope_append_paged */
+  int layout;
+} attn_paged_cache_t;
+
+/*
+ * Block tables and slot maps of the next step, built on the device from the
+ * requests' lengths (one kernel).  Request b holds past_lens[b] keys in its
+ * first ceil(past_lens[b] / page_size) table entries and brings new_lens[b] >= 0
+ * tokens; the tokens of all requests lie one after the other in a ragged batch
+ * of T >= sum new_lens tokens, of which those behind the last request are
+ * padding.
+ *   free_pages   device int32 [num_free]; its entries free_range[0] ..
+ *                free_range[1] - 1 are the free pages, taken from the front:
+ *                requests are served in order, request b while the pages that
+ *                requests 0 .. b need together are no more than the free ones
+ *                (one that needs no new page always is).
+ *   block_table  device int32 [B, max_pages]: new entries are written, no other.
+ *   cu_new       [B + 1]: first token of each request, cu_new[B] = the tokens.
+ *   total_lens   [B]: past_lens[b] + new_lens[b]; past_lens[b] where refused.
+ *   positions    [T]: past_lens[b] + index in the request; -1 for padding.
+ *   slot_map     [T]: the token's slot; -1 for padding and refused requests.
+ *   free_range_out [2]: free_range with the pages taken removed.
+ * total_lens may be past_lens or new_lens, and free_range_out may be
+ * free_range (advanced in place); the buffers must not overlap otherwise.  A
+ * request is refused, and ATTN_ERR_PAGE reported by attn_check_device_error,
+ * when a length is negative, past + new exceeds max_pages * page_size, its
+ * tokens end behind T (cu_new is then held at T), or the free pages do not
+ * suffice.  A request refused for its pages keeps its tokens' places and
+ * positions.  B at most 16384, T at most 2^30.  All pointers 4-byte aligned
+ * (16-byte aligned positions and slot_map are written faster).  Errors:
+ * ATTN_ERR_SHAPE, ATTN_ERR_NULL, ATTN_ERR_ALIGN, ATTN_ERR_PAGE (page_size).
+ */
+attn_status_t attn_page_plan(const int* past_lens, const int* new_lens, int* block_table, const int* free_pages,
+                             const int* free_range, int* cu_new, int* total_lens, int* positions, int* slot_map,
+                             int* free_range_out, int B, int max_pages, int num_free, int page_size, int T,
+                             void* stream);
+
+/*
+ * attn_rope_append for a ragged batch and a paged cache: token t of the T
+ * tokens is rotated at positions[t] and its k and v go to slot slot_map[t]
+ * (attn_page_plan makes both).
+ *   packed_qkv  [T, (Hq + 2*Hkv) * d] bf16, q heads, then k, then v
+ *   q_out       [T, Hq, d] bf16
+ * A token with a negative slot is skipped: its row of q_out stays as it was.
+ * So is one whose position is outside [0, max_pos) (ATTN_ERR_SEQLEN is
+ * reported) or whose slot is behind the last page (ATTN_ERR_PAGE).  The slots
+ * that are not negative must differ from one another.  Other arguments and
+ * errors as attn_rope_append; ATTN_ERR_PAGE for a bad page_size or page_stride.
+ */
+attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_table, const float* sin_table,
+                                     int max_pos, const int* positions, const int* slot_map, void* q_out,
+                                     const attn_paged_cache_t* cache, int T, int Hq, int Hkv, int d, void* stream);
+
+/*
+ * Attention of chunks of new tokens over a paged cache (prompts, their chunks,
+ * and single tokens mixed in one ragged batch):
+ *   q, o       [T, Hq, d] bf16; sequence b's tokens are cu_q[b] .. cu_q[b+1] - 1
+ *   cu_q       device int32 [B + 1], non-decreasing, cu_q[B] <= T
+ *   seqlens_k  device int32 [B]: its keys, the new tokens' own among them
+ *   lse        [Hq, T] fp32 or NULL
+ * Token i of the n_b tokens of sequence b sees key j < seqlens_k[b], under
+ * ATTN_CAUSAL_BOTTOM_RIGHT iff j <= i + seqlens_k[b] - n_b, under
+ * ATTN_CAUSAL_TOP_LEFT iff j <= i.  A token that sees no key gets o = 0 and
+ * lse = -inf.  Rows behind cu_q[B] are left as they were.  A length outside
+ * [0, max_pages * page_size] or a cu_q that decreases or passes T is clamped
+ * and reported (ATTN_ERR_SEQLEN); a page id outside [0, num_pages) reads as a
+ * page of zeros and is reported (ATTN_ERR_PAGE).
+ *   workspace  attn_fwd_paged_workspace_size(...) bytes, device, 16-byte
+ *              aligned, caller-owned; nothing in it needs to be initialised,
+ *              and calls that may overlap on the GPU need one each.
+ * Errors as attn_fwd, plus ATTN_ERR_WORKSPACE and ATTN_ERR_PAGE.
+ */
+size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d);
+attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, const int* cu_q, const int* seqlens_k,
+                             void* o, float* lse, int B, int T, int Hq, int Hkv, int d, float scale, int causal,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Split-KV decode over a paged cache: Sq new tokens for each of B sequences.
+ *   q, o       [B, Sq, Hq, d] bf16 (the token-major order attn_rope_append_paged
+ *              writes); lse [B, Hq, Sq] fp32 or NULL
+ *   seqlens_k  device int32 [B]: keys per sequence, the new tokens' among them
+ * Masks, clamping, pages and workspace as attn_fwd_paged.
+ */
+size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Sq, int d);
+attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t* cache, const int* seqlens_k, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int Sq, int d, float scale, int causal,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Self-test of the bounded-wait contract above (not a computation): runs the
  * split-KV decode of attn_decode_splitkv (bottom-right mask, default scale,
  * automatic split count) with its K/V copies withheld, so every consumer
@@ -363,9 +479,10 @@ const char* attn_status_string(attn_status_t status);
 /*
  * Synchronizes `stream`, then reads and clears the device error word.
  * Returns ATTN_ERR_DEVICE_TIMEOUT if a kernel gave up on a bounded wait since
- * the last check, else ATTN_ERR_SEQLEN if attn_fwd_varlen or
- * attn_decode_splitkv_varlen had to clamp a per-batch length or
- * attn_rope_append skipped a token, ATTN_ERR_CUDA
+ * the last check, else ATTN_ERR_PAGE if a page id, slot or page request was out of
+ * range, else ATTN_ERR_SEQLEN if attn_fwd_varlen, attn_decode_splitkv_varlen
+ * or a paged entry point had to clamp a length or attn_rope_append skipped a
+ * token, ATTN_ERR_CUDA
  * if the synchronization itself failed, else ATTN_OK.
  */
 attn_status_t attn_check_device_error(void* stream);

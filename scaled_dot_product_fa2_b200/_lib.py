@@ -16,11 +16,13 @@ STATUS_NAMES = {
     0: "ATTN_OK", 1: "ATTN_ERR_NULL", 2: "ATTN_ERR_SHAPE", 3: "ATTN_ERR_GQA", 4: "ATTN_ERR_HEADDIM",
     5: "ATTN_ERR_ALIGN", 6: "ATTN_ERR_CAUSAL", 7: "ATTN_ERR_WORKSPACE", 8: "ATTN_ERR_CUDA",
     9: "ATTN_ERR_DEVICE_TIMEOUT", 10: "ATTN_ERR_ARCH", 11: "ATTN_ERR_SCALE", 12: "ATTN_ERR_SCRATCH_LIMIT",
-    13: "ATTN_ERR_SEQLEN",
+    13: "ATTN_ERR_SEQLEN", 14: "ATTN_ERR_PAGE",
 }
 STATIC_SCRATCH_BYTES = 16 << 20
 EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_fwd_varlen", "attn_decode_num_splits", "attn_decode_workspace_size", "attn_decode_splitkv",
            "attn_decode_splitkv_varlen", "attn_decode_splitkv_ex", "attn_decode_splitkv_static", "attn_rope_append", "attn_bwd", "attn_bwd_workspace_size",
+           "attn_page_plan", "attn_rope_append_paged", "attn_fwd_paged", "attn_fwd_paged_workspace_size",
+           "attn_decode_splitkv_paged", "attn_decode_paged_workspace_size",
            "attn_selftest_decode_wait_timeout", "attn_status_string",
            "attn_check_device_error", "attn_version")
 
@@ -28,6 +30,13 @@ class Extras(ctypes.Structure):
     """attn_extras_t of the C ABI."""
     _fields_ = [("seqlens_q", ctypes.c_void_p), ("seqlens_k", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("bias_b", ctypes.c_int), ("bias_h", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class PagedCache(ctypes.Structure):
+    """attn_paged_cache_t of the C ABI."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("layout", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -72,6 +81,19 @@ def _declare(lib):
     lib.attn_bwd.restype = I
     lib.attn_bwd_workspace_size.argtypes = [I, I, I]
     lib.attn_bwd_workspace_size.restype = SZ
+    PC = ctypes.POINTER(PagedCache)
+    lib.attn_page_plan.argtypes = [P] * 10 + [I] * 5 + [P]
+    lib.attn_page_plan.restype = I
+    lib.attn_rope_append_paged.argtypes = [P, P, P, I, P, P, P, PC, I, I, I, I, P]
+    lib.attn_rope_append_paged.restype = I
+    lib.attn_fwd_paged.argtypes = [P, PC, P, P, P, P, I, I, I, I, I, F, I, P, SZ, P]
+    lib.attn_fwd_paged.restype = I
+    lib.attn_fwd_paged_workspace_size.argtypes = [I, I, I, I]
+    lib.attn_fwd_paged_workspace_size.restype = SZ
+    lib.attn_decode_splitkv_paged.argtypes = [P, PC, P, P, P, I, I, I, I, I, F, I, P, SZ, P]
+    lib.attn_decode_splitkv_paged.restype = I
+    lib.attn_decode_paged_workspace_size.argtypes = [I, I, I, I, I]
+    lib.attn_decode_paged_workspace_size.restype = SZ
     lib.attn_selftest_decode_wait_timeout.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P, SZ, P]
     lib.attn_selftest_decode_wait_timeout.restype = I
     lib.attn_status_string.argtypes = [I]

@@ -1,0 +1,248 @@
+// paged_host.cuh -- host side of the paged KV cache's entry points: argument
+// checks and launches.  Included by sdpa_b200.cu after the shared helpers.
+#pragma once
+
+namespace sdpa {
+namespace {
+
+constexpr int kMinPage = 16, kMaxPage = 256;
+
+bool page_size_ok(int P) { return P >= kMinPage && P <= kMaxPage && (P & (P - 1)) == 0; }
+
+int log2_of(int P) {
+  int s = 0;
+  while ((1 << s) < P) ++s;
+  return s;
+}
+
+// Checks of a paged cache; the strides (page, head, row) in elements.
+attn_status_t check_cache(const attn_paged_cache_t* c, int Hkv, int d, bool has_table, int64_t* sp, int64_t* sh,
+                          int64_t* sr) {
+  if (c == nullptr) return ATTN_ERR_NULL;
+  if (c->num_pages < 0 || (has_table && c->max_pages < 0)) return ATTN_ERR_SHAPE;
+  if (c->layout != ATTN_LAYOUT_BHSD && c->layout != ATTN_LAYOUT_BSHD) return ATTN_ERR_SHAPE;
+  if (!page_size_ok(c->page_size)) return ATTN_ERR_PAGE;
+  if (static_cast<int64_t>(c->num_pages) * c->page_size > (int64_t{1} << 31)) return ATTN_ERR_SHAPE;
+  if (has_table && static_cast<int64_t>(c->max_pages) * c->page_size > kMaxSeq) return ATTN_ERR_SHAPE;
+  const int64_t dense = static_cast<int64_t>(Hkv) * c->page_size * d;
+  if (c->page_stride != 0 && (c->page_stride < dense || c->page_stride % 8 != 0)) return ATTN_ERR_PAGE;
+  // a tensor map's strides are below 2^40 bytes
+  if (c->page_stride >= (int64_t{1} << 38) || dense >= (int64_t{1} << 38)) return ATTN_ERR_SHAPE;
+  if (c->num_pages > 0) {
+    if (c->k_pages == nullptr || c->v_pages == nullptr) return ATTN_ERR_NULL;
+    if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return ATTN_ERR_ALIGN;
+  }
+  if (has_table && c->max_pages > 0) {
+    if (c->block_table == nullptr) return ATTN_ERR_NULL;
+    if (!aligned(c->block_table, 4)) return ATTN_ERR_ALIGN;
+  }
+  *sp = c->page_stride != 0 ? c->page_stride : dense;
+  const Strides s = layout_strides(c->layout, Hkv, c->page_size, d);
+  *sh = s.h;
+  *sr = s.r;
+  return ATTN_OK;
+}
+
+// Checks that attn_fwd_paged and attn_decode_splitkv_paged share, and the
+// parameters that do not depend on the entry point.
+attn_status_t paged_params(PagedParams* p, const void* q, const attn_paged_cache_t* cache, const int* lens, void* o,
+                           float* lse, int B, int64_t T, int Hq, int Hkv, int d, float scale, int causal) {
+  if (B < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return ATTN_ERR_SHAPE;
+  if (T > kMaxSeq || B > kMaxSeq || Hq > (1 << 20)) return ATTN_ERR_SHAPE;
+  if (Hq % Hkv != 0) return ATTN_ERR_GQA;
+  if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
+  if (causal < ATTN_CAUSAL_NONE || causal > ATTN_CAUSAL_BOTTOM_RIGHT) return ATTN_ERR_CAUSAL;
+  if (!(scale >= 0.f) || std::isinf(scale)) return ATTN_ERR_SCALE;
+  std::memset(p, 0, sizeof(*p));
+  const attn_status_t s = check_cache(cache, Hkv, d, true, &p->sp, &p->sh, &p->sr);
+  if (s != ATTN_OK) return s;
+  if (B > 0 && T > 0) {
+    if (q == nullptr || o == nullptr || lens == nullptr) return ATTN_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lens, 4)) return ATTN_ERR_ALIGN;
+    if (lse != nullptr && !aligned(lse, 4)) return ATTN_ERR_ALIGN;
+  }
+  p->q = static_cast<const uint16_t*>(q);
+  p->k = static_cast<const uint16_t*>(cache->k_pages);
+  p->v = static_cast<const uint16_t*>(cache->v_pages);
+  p->o = static_cast<uint16_t*>(o);
+  p->lse = lse;
+  p->lens = lens;
+  p->table = cache->block_table;
+  p->B = B;
+  p->T = static_cast<int>(T);
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->group = Hq / Hkv;
+  p->num_pages = cache->num_pages;
+  p->max_pages = cache->max_pages;
+  p->page_shift = log2_of(cache->page_size);
+  p->causal = causal;
+  p->scale = effective_scale(scale, d);
+  p->scale_log2 = p->scale * 1.4426950408889634f;
+  return ATTN_OK;
+}
+
+attn_status_t launch_paged_rows(const PagedParams& p, int d, cudaStream_t st) {
+  const int64_t blocks = (static_cast<int64_t>(p.T) * p.Hq + 7) / 8;
+  if (blocks > INT_MAX) return ATTN_ERR_SHAPE;
+  if (d == 128) paged_rows_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  else paged_rows_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sdpa
+
+extern "C" {
+
+attn_status_t attn_page_plan(const int* past_lens, const int* new_lens, int* block_table, const int* free_pages,
+                             const int* free_range, int* cu_new, int* total_lens, int* positions, int* slot_map,
+                             int* free_range_out, int B, int max_pages, int num_free, int page_size, int T,
+                             void* stream) {
+  if (B < 0 || max_pages < 0 || num_free < 0 || T < 0) return ATTN_ERR_SHAPE;
+  if (B > kPlanMaxBatch || T > kMaxSeq) return ATTN_ERR_SHAPE;
+  if (!page_size_ok(page_size)) return ATTN_ERR_PAGE;
+  if (static_cast<int64_t>(max_pages) * page_size > kMaxSeq) return ATTN_ERR_SHAPE;
+  if (cu_new == nullptr || free_range == nullptr || free_range_out == nullptr) return ATTN_ERR_NULL;
+  if (B > 0 && (past_lens == nullptr || new_lens == nullptr || total_lens == nullptr)) return ATTN_ERR_NULL;
+  if (B > 0 && max_pages > 0 && block_table == nullptr) return ATTN_ERR_NULL;
+  if (num_free > 0 && free_pages == nullptr) return ATTN_ERR_NULL;
+  if (T > 0 && (positions == nullptr || slot_map == nullptr)) return ATTN_ERR_NULL;
+  for (const void* ptr : {static_cast<const void*>(past_lens), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_range), static_cast<const void*>(cu_new),
+                          static_cast<const void*>(total_lens), static_cast<const void*>(positions),
+                          static_cast<const void*>(slot_map), static_cast<const void*>(free_range_out)})
+    if (!aligned(ptr, 4)) return ATTN_ERR_ALIGN;
+  int dev = 0;
+  attn_status_t s = current_device(&dev, nullptr);
+  if (s != ATTN_OK) return s;
+  PlanParams p;
+  p.past = past_lens;
+  p.fresh = new_lens;
+  p.table = block_table;
+  p.free_pages = free_pages;
+  p.free_range = free_range;
+  p.cu = cu_new;
+  p.total = total_lens;
+  p.positions = positions;
+  p.slots = slot_map;
+  p.range_out = free_range_out;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.num_free = num_free;
+  p.T = T;
+  p.page_shift = log2_of(page_size);
+  static bool smem_done[kMaxDevices] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set_smem(page_plan_kernel, plan_smem_bytes(kPlanMaxBatch), dev, smem_done)) return ATTN_ERR_CUDA;
+  }
+  // one cluster, just wide enough for one pass over the tokens
+  int ctas = 1;
+  while (ctas < kPlanMaxCluster && static_cast<int64_t>(ctas) * kPlanThreads * kPlanTokens < T) ctas *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(plan_smem_bytes(B));
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_plan_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_table, const float* sin_table,
+                                     int max_pos, const int* positions, const int* slot_map, void* q_out,
+                                     const attn_paged_cache_t* cache, int T, int Hq, int Hkv, int d, void* stream) {
+  if (T < 0 || Hq <= 0 || Hkv <= 0 || max_pos <= 0) return ATTN_ERR_SHAPE;
+  if (T > kMaxSeq || max_pos > kMaxSeq || Hq + 2 * static_cast<int64_t>(Hkv) > INT_MAX / 128) return ATTN_ERR_SHAPE;
+  if (Hq % Hkv != 0) return ATTN_ERR_GQA;
+  if (d != 64 && d != 128) return ATTN_ERR_HEADDIM;
+  RopeParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  attn_status_t s = check_cache(cache, Hkv, d, false, &prm.c_sb, &prm.c_sh, &prm.c_sr);
+  if (s != ATTN_OK) return s;
+  if (T == 0) return ATTN_OK;
+  if (packed_qkv == nullptr || cos_table == nullptr || sin_table == nullptr || q_out == nullptr ||
+      positions == nullptr || slot_map == nullptr)
+    return ATTN_ERR_NULL;
+  if (!aligned(packed_qkv, 16) || !aligned(cos_table, 16) || !aligned(sin_table, 16) || !aligned(q_out, 16) ||
+      !aligned(positions, 4) || !aligned(slot_map, 4))
+    return ATTN_ERR_ALIGN;
+  int sms = 0;
+  if ((s = current_device(nullptr, &sms)) != ATTN_OK) return s;
+  prm.packed = static_cast<const uint16_t*>(packed_qkv);
+  prm.cos_t = cos_table;
+  prm.sin_t = sin_table;
+  prm.q_out = static_cast<uint16_t*>(q_out);
+  prm.k_cache = static_cast<uint16_t*>(cache->k_pages);
+  prm.v_cache = static_cast<uint16_t*>(cache->v_pages);
+  prm.q_sh = d;
+  prm.q_sr = static_cast<int64_t>(Hq) * d;
+  prm.tokens = T;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.max_pos = max_pos;
+  prm.positions = positions;
+  prm.slots = slot_map;
+  prm.page_shift = log2_of(cache->page_size);
+  prm.num_pages = cache->num_pages;
+  const int grid = static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * kRopeBlocksPerSm));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 128) rope_append_kernel<128, true><<<grid, kRopeWarps * 32, 0, st>>>(prm);
+  else rope_append_kernel<64, true><<<grid, kRopeWarps * 32, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {
+  if (T < 0 || T > kMaxSeq || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return 16;
+}
+
+attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, const int* cu_q, const int* seqlens_k,
+                             void* o, float* lse, int B, int T, int Hq, int Hkv, int d, float scale, int causal,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  PagedParams p;
+  attn_status_t s = paged_params(&p, q, cache, seqlens_k, o, lse, B, T, Hq, Hkv, d, scale, causal);
+  if (s != ATTN_OK) return s;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (cu_q == nullptr) return ATTN_ERR_NULL;
+  if (!aligned(cu_q, 4)) return ATTN_ERR_ALIGN;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
+    return ATTN_ERR_WORKSPACE;
+  if ((s = current_device(nullptr, nullptr)) != ATTN_OK) return s;
+  p.cu_q = cu_q;
+  return launch_paged_rows(p, d, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
+  if (B < 0 || Sq < 0 || static_cast<int64_t>(B) * Sq > kMaxSeq || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
+      (d != 64 && d != 128))
+    return 0;
+  return 16;
+}
+
+attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t* cache, const int* seqlens_k, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int Sq, int d, float scale, int causal,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || Sq < 0) return ATTN_ERR_SHAPE;
+  PagedParams p;
+  attn_status_t s = paged_params(&p, q, cache, seqlens_k, o, lse, B, static_cast<int64_t>(B) * Sq, Hq, Hkv, d, scale,
+                                 causal);
+  if (s != ATTN_OK) return s;
+  if (B == 0 || Sq == 0) return ATTN_OK;
+  if (workspace == nullptr || !aligned(workspace, 16) ||
+      workspace_bytes < attn_decode_paged_workspace_size(B, Hq, Hkv, Sq, d))
+    return ATTN_ERR_WORKSPACE;
+  if ((s = current_device(nullptr, nullptr)) != ATTN_OK) return s;
+  p.Sq = Sq;
+  return launch_paged_rows(p, d, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

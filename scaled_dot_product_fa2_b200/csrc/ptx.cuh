@@ -15,11 +15,13 @@ namespace sdpa {
 // Device-side error word of the library (one per device; the library is a
 // single translation unit, so it is defined here).  Bit kErrWaitTimeout is set
 // when a bounded wait gives up; bit kErrSeqlen when a kernel had to clamp a
-// per-batch key length read from device memory.
+// per-batch key length read from device memory; bit kErrPage when a page, a slot
+// or a page plan's request was out of range.
 __device__ unsigned int g_error_word = 0;
 
 constexpr unsigned int kErrWaitTimeout = 1u;
 constexpr unsigned int kErrSeqlen = 2u;  // a per-batch key length was outside [0, cache capacity]
+constexpr unsigned int kErrPage = 4u;    // a page id, slot or page request out of range
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -306,6 +308,12 @@ __device__ __forceinline__ void grid_dependency_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Every thread of every CTA of the cluster; orders their memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

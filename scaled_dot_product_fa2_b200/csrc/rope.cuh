@@ -21,6 +21,12 @@
 // shuffle.  Tokens are pipelined one deep: a block issues the loads of its
 // next token's rows before it rotates and stores the current token's, so its
 // loads never wait for its stores (at 64 registers, four blocks per SM).
+//
+// PAGED: the cache is a pool of pages of P rows.  Token bt of a ragged batch
+// has its position and its slot (page * P + row) in two arrays; the page takes
+// the batch's place in the cache strides, and q keeps the token-major layout
+// [T, Hq, d].  A negative slot marks a token without a place: nothing of it is
+// written.
 #pragma once
 #include <climits>
 
@@ -42,6 +48,11 @@ struct RopeParams {
   int64_t c_sb, c_sh, c_sr;
   int tokens;              // B * S_new (< 2^31, checked on the host)
   int B, S_new, Hq, Hkv, cap, max_pos;
+  // paged cache (c_sb, c_sh, c_sr: page, head and row strides; q_sb = 0)
+  const int* positions;    // [tokens]
+  const int* slots;        // [tokens]
+  int page_shift;          // log2 P
+  int num_pages;
 };
 
 constexpr int kRopeWarps = 8;        // warps per block (256 threads)
@@ -65,7 +76,7 @@ __global__ void rope_lengths_kernel(const int* past_lens, int* total_lens, int B
   }
 }
 
-template <int D>
+template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
     rope_append_kernel(const __grid_constant__ RopeParams p) {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
@@ -85,11 +96,27 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
 
   // Safe only because total_lens never overlaps past_lens here (the host
   // then leaves total_lens to rope_lengths_kernel, launched after this one).
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.B; i += gridDim.x * blockDim.x)
-    if (p.total_lens != nullptr) p.total_lens[i] = rope_total_length(__ldg(p.past_lens + i), p.S_new);
+  if constexpr (!PAGED) {
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.B; i += gridDim.x * blockDim.x)
+      if (p.total_lens != nullptr) p.total_lens[i] = rope_total_length(__ldg(p.past_lens + i), p.S_new);
+  }
 
-  // Token bt's position, or -1 when it is out of range (reported, skipped).
-  auto token_pos = [&](int bt, int& b, int& t) {
+  // Token bt's position, or -1 when it is out of range (reported, skipped);
+  // its cache row is `row` of batch (or page) b.
+  auto token_pos = [&](int bt, int& b, int& t, int& row) {
+    if constexpr (PAGED) {
+      t = bt;
+      const int slot = __ldg(p.slots + bt);
+      const int pos = __ldg(p.positions + bt);
+      b = slot >> p.page_shift;
+      row = slot & ((1 << p.page_shift) - 1);
+      if (slot < 0) return -1;  // no place: nothing to report
+      if (b >= p.num_pages || pos < 0 || pos >= p.max_pos) {
+        if (threadIdx.x == 0) atomicOr(&g_error_word, b >= p.num_pages ? kErrPage : kErrSeqlen);
+        return -1;
+      }
+      return pos;
+    }
     b = bt / p.S_new;
     t = bt - b * p.S_new;
     const int past = __ldg(p.past_lens + b);
@@ -99,6 +126,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
       if (threadIdx.x == 0) atomicOr(&g_error_word, kErrSeqlen);
       return -1;
     }
+    row = past + t;
     return past + t;
   };
   // The loads of one token's head rows (kRopeUnroll block passes cover every
@@ -113,10 +141,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
     }
   };
   // Rotate and store the rows of one round.
-  auto store_rows = [&](int b, int t, int pos, int h0, const uint4 (&x)[kRopeUnroll], const float (&c)[8],
+  auto store_rows = [&](int b, int t, int row, int h0, const uint4 (&x)[kRopeUnroll], const float (&c)[8],
                         const float (&s)[8]) {
     uint16_t* const q_base = p.q_out + b * p.q_sb + t * p.q_sr;
-    const int64_t c_off = b * p.c_sb + static_cast<int64_t>(pos) * p.c_sr;
+    const int64_t c_off = b * p.c_sb + static_cast<int64_t>(row) * p.c_sr;
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
       // every lane of the warp takes part in the exchange; the partner lane
@@ -156,16 +184,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
   // of a block never stop for its stores.
   int bt = blockIdx.x;  // block-uniform
   if (bt >= p.tokens) return;
-  int b, t;
-  int pos = token_pos(bt, b, t);
+  int b, t, row = 0;
+  int pos = token_pos(bt, b, t, row);
   uint4 x[kRopeUnroll];
   if (pos >= 0) load_rows(bt, 0, x);
   while (true) {
     const int nbt = bt + gridDim.x;
-    int nb = 0, nt = 0, npos = -1;
+    int nb = 0, nt = 0, nrow = 0, npos = -1;
     uint4 xn[kRopeUnroll];
     if (nbt < p.tokens) {
-      npos = token_pos(nbt, nb, nt);
+      npos = token_pos(nbt, nb, nt, nrow);
       if (npos >= 0) load_rows(nbt, 0, xn);
     }
     if (pos >= 0) {
@@ -175,17 +203,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
       const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
       const float s[8] = {s0.x * sign, s0.y * sign, s0.z * sign, s0.w * sign,
                           s1.x * sign, s1.y * sign, s1.z * sign, s1.w * sign};
-      store_rows(b, t, pos, 0, x, c, s);
+      store_rows(b, t, row, 0, x, c, s);
       for (int h0 = kBlockRows * kRopeUnroll; h0 < slots; h0 += kBlockRows * kRopeUnroll) {  // block-uniform
         uint4 xr[kRopeUnroll];
         load_rows(bt, h0, xr);
-        store_rows(b, t, pos, h0, xr, c, s);
+        store_rows(b, t, row, h0, xr, c, s);
       }
     }
     if (nbt >= p.tokens) break;
     bt = nbt;
     b = nb;
     t = nt;
+    row = nrow;
     pos = npos;
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) x[u] = xn[u];

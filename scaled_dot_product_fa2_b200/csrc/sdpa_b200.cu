@@ -16,6 +16,8 @@
 #include "prefill.cuh"
 #include "rope.cuh"
 #include "backward.cuh"
+#include "page_plan.cuh"
+#include "paged.cuh"
 
 namespace sdpa {
 constexpr int kMaxDeviceSlots = 64;
@@ -810,6 +812,7 @@ const char* attn_status_string(attn_status_t status) {
     case ATTN_ERR_ARCH: return "the current device is not sm_100 (B200)";
     case ATTN_ERR_SCALE: return "scale must be 0 (default) or finite and > 0";
     case ATTN_ERR_SCRATCH_LIMIT: return "problem needs more than the library's static decode scratch (16 MiB)";
+    case ATTN_ERR_PAGE: return "a page size, page id, slot or page request was out of range";
     case ATTN_ERR_SEQLEN: return "a per-batch length or position was outside its range (clamped or skipped)";
   }
   return "unknown status";
@@ -822,7 +825,8 @@ attn_status_t attn_check_device_error(void* stream) {
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(sdpa::g_error_word, &zero, sizeof(zero)) != cudaSuccess) return ATTN_ERR_CUDA;
-    return (word & sdpa::kErrWaitTimeout) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_ERR_SEQLEN;
+    if (word & sdpa::kErrWaitTimeout) return ATTN_ERR_DEVICE_TIMEOUT;
+    return (word & sdpa::kErrPage) ? ATTN_ERR_PAGE : ATTN_ERR_SEQLEN;
   }
   return ATTN_OK;
 }
@@ -830,6 +834,8 @@ attn_status_t attn_check_device_error(void* stream) {
 int attn_version(void) { return 100; }
 
 }  // extern "C"
+
+#include "paged_host.cuh"
 
 // ---------------------------------------------------------------- allocation-free decode
 // Scratch for attn_decode_splitkv_static: a file-scope device array, so the
