@@ -82,6 +82,53 @@ attn_status_t paged_params(PagedParams* p, const void* q, const attn_paged_cache
   return ATTN_OK;
 }
 
+// 5-D map (64 columns, page row, 64-column block, head, page) over a pool of pages; box {64, rows,
+// d/64, 1, 1}: one copy brings `rows` rows of a page as d/64 blocks of 128-byte swizzled rows.
+// Without pages the map has one (of `base`, never read: its index is not a valid one).
+bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int d, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[5] = {64, cuuint64_t{1} << p.page_shift, static_cast<cuuint64_t>(d / 64),
+                              static_cast<cuuint64_t>(p.Hkv), static_cast<cuuint64_t>(std::max(p.num_pages, 1))};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(p.sr) * 2, 128, static_cast<cuuint64_t>(p.sh) * 2,
+                                 static_cast<cuuint64_t>(p.sp) * 2};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(d / 64), 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The decode's workspace: two partial row sets and one join per CTA of the grid.
+size_t paged_decode_ws_bytes(int sms, int d) {
+  return static_cast<size_t>(sms) * (2 * kPdRows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
+                                     sizeof(int4));
+}
+
+template <int D>
+attn_status_t launch_paged_decode(const PagedDecodeParams& a, int sms, int dev, cudaStream_t st) {
+  static bool smem_done[kMaxDevices] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set_smem(paged_decode_kernel<D>, PagedDecodeCfg<D>::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kPdThreads);
+  cfg.dynamicSmemBytes = PagedDecodeCfg<D>::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+  cfg.blockDim = dim3(kPdRows * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 attn_status_t launch_paged_rows(const PagedParams& p, int d, cudaStream_t st) {
   const int64_t blocks = (static_cast<int64_t>(p.T) * p.Hq + 7) / 8;
   if (blocks > INT_MAX) return ATTN_ERR_SHAPE;
@@ -225,24 +272,39 @@ size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
   if (B < 0 || Sq < 0 || static_cast<int64_t>(B) * Sq > kMaxSeq || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
       (d != 64 && d != 128))
     return 0;
-  return 16;
+  return paged_decode_ws_bytes(sm_count_or_default(), d);
 }
 
 attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t* cache, const int* seqlens_k, void* o,
                                         float* lse, int B, int Hq, int Hkv, int Sq, int d, float scale, int causal,
                                         void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || Sq < 0) return ATTN_ERR_SHAPE;
-  PagedParams p;
-  attn_status_t s = paged_params(&p, q, cache, seqlens_k, o, lse, B, static_cast<int64_t>(B) * Sq, Hq, Hkv, d, scale,
+  PagedDecodeParams a;
+  attn_status_t s = paged_params(&a.p, q, cache, seqlens_k, o, lse, B, static_cast<int64_t>(B) * Sq, Hq, Hkv, d, scale,
                                  causal);
   if (s != ATTN_OK) return s;
   if (B == 0 || Sq == 0) return ATTN_OK;
   if (workspace == nullptr || !aligned(workspace, 16) ||
       workspace_bytes < attn_decode_paged_workspace_size(B, Hq, Hkv, Sq, d))
     return ATTN_ERR_WORKSPACE;
-  if ((s = current_device(nullptr, nullptr)) != ATTN_OK) return s;
-  p.Sq = Sq;
-  return launch_paged_rows(p, d, static_cast<cudaStream_t>(stream));
+  int dev = 0, sms = 0;
+  if ((s = current_device(&dev, &sms)) != ATTN_OK) return s;
+  a.p.Sq = Sq;
+  const int64_t rows = static_cast<int64_t>(a.p.group) * Sq;
+  if (rows > INT_MAX / 2) return ATTN_ERR_SHAPE;
+  a.row_groups = static_cast<int>((rows + kPdRows - 1) / kPdRows);
+  if (static_cast<int64_t>(Hkv) * a.row_groups > INT_MAX / 2) return ATTN_ERR_SHAPE;
+  const bool pages = a.p.num_pages > 0;
+  a.oob_page = std::max(a.p.num_pages, 1);
+  const int box = std::min(1 << a.p.page_shift, kPdKeys);
+  if (!make_page_map(&a.tm_k, pages ? cache->k_pages : q, a.p, d, box) ||
+      !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box))
+    return ATTN_ERR_CUDA;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * sms) * kPdRows * d);
+  a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(2 * sms) * kPdRows);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_paged_decode<128>(a, sms, dev, st) : launch_paged_decode<64>(a, sms, dev, st);
 }
 
 }  // extern "C"

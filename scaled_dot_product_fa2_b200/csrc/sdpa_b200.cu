@@ -18,6 +18,7 @@
 #include "backward.cuh"
 #include "page_plan.cuh"
 #include "paged.cuh"
+#include "paged_decode.cuh"
 
 namespace sdpa {
 constexpr int kMaxDeviceSlots = 64;

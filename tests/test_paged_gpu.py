@@ -560,3 +560,31 @@ def test_two_streams_with_a_workspace_each(sdpa):
         for o, lse in outs[i]:
             check(o, lse, refs[i])
     sdpa.check_device_error()
+
+
+@pytest.mark.parametrize("page,d", [(64, 128), (16, 64)])
+def test_many_decodes_in_a_row_over_large_caches(sdpa, page, d):
+    """Back-to-back calls over caches that do not fit the L2 together: copies land in any order, and
+    each call's first copies are in flight while the call before it ends."""
+    B, Hq, Hkv, L = 8, 32, 8, 8192
+    N, W = B * L // page, L // page
+    gen = torch.Generator(device="cuda").manual_seed(page)
+    sets = []
+    for _ in range(3):
+        k, v = (torch.randn((N, Hkv, page, d), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        table = torch.randperm(N, generator=gen, device="cuda").int().view(B, W)
+        q = torch.randn((B, 1, Hq, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+        sets.append((q, k, v, ints([L - 13 * i for i in range(B)]), table, sdpa.decode_paged_workspace(q, k)))
+    first = []
+    for q, k, v, lens, table, ws in sets:
+        o, lse = sdpa.attn_decode_splitkv_paged(q, k, v, lens, table, workspace=ws)
+        keys = k[table[3, :].long()].transpose(1, 2).reshape(-1, Hkv, d)[:lens[3].item()].double()
+        s = torch.einsum("hgd,khd->hgk", q[3, 0].double().view(Hkv, Hq // Hkv, d), keys) / d ** 0.5
+        assert (torch.logsumexp(s, -1).flatten() - lse[3, :, 0].double()).abs().max() < 1e-4
+        first.append((o, lse))
+    for i in range(600):
+        q, k, v, lens, table, ws = sets[i % 3]
+        o, lse = sdpa.attn_decode_splitkv_paged(q, k, v, lens, table, workspace=ws)
+        if i % 50 >= 47:
+            assert torch.equal(o, first[i % 3][0]) and torch.equal(lse, first[i % 3][1])
+    sdpa.check_device_error()
