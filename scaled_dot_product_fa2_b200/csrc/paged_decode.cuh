@@ -6,9 +6,10 @@
 // two products per key for at most 16 rows, so its floor is the bytes of the
 // valid keys and values, and all of the design serves the memory system:
 //   * All items' tiles form one line, in the order (sequence, head, row
-//     group), and the grid -- one CTA per SM -- cuts it into equal shares.
+//     group), and the grid -- two CTAs per SM -- cuts it into equal shares.
 //     A share may begin and end inside an item, so the longest CTA does one
-//     tile more than the shortest, whatever the lengths are.  The line is
+//     tile more than the shortest, whatever the lengths are.  An item's fixed
+//     cost takes kPdItemCost places on the line before its tiles.  The line is
 //     measured on the device: every CTA sums the tile counts for itself and
 //     finds its first item; nothing about the lengths is known on the host.
 //   * One producer warp streams K/V tiles through a ring of kStages slots and
@@ -16,10 +17,10 @@
 //     flight while an item's result is merged and written.  One TMA copy
 //     brings a page's (at most 64) rows; the lanes issue a tile's copies side
 //     by side, each with the table entry it read one tile ahead.
-//   * Eight consumer warps, in two sets of four that take tiles in turn; a
-//     warp owns 16 keys of a tile and its own (max, sum, output), on
-//     mma.sync m16n8k16 (the tensor pipe is idle most of the time either
-//     way).  An item's end merges the eight through shared memory.
+//   * Four consumer warps; a warp owns 16 keys of every tile and its own (max,
+//     sum, output), on mma.sync m16n8k16 (the tensor pipe is idle most of the
+//     time either way).  An item's end merges the four through shared memory;
+//     the other CTA of the SM streams meanwhile.
 //   * An item inside one share is written as it is.  One that crosses shares
 //     leaves an fp32 partial row set per CTA -- at most two per CTA, one for
 //     an item it ends or passes through, one for an item it begins -- and a
@@ -32,9 +33,11 @@ namespace sdpa {
 
 constexpr int kPdKeys = 64;                 // keys per tile
 constexpr int kPdRows = 16;                 // query rows per item (mma M)
-constexpr int kPdWarps = 8;                 // consumer warps
+constexpr int kPdWarps = 4;                 // consumer warps, 16 keys of a tile each
+constexpr int kPdCtasPerSm = 2;
 constexpr int kPdThreads = kPdWarps * 32 + 32;
 constexpr int kPdSegRing = 4;               // pieces announced ahead by the producer
+constexpr int kPdItemCost = 2;              // an item's fixed cost (query loads, merge, writes) in tiles
 
 struct PagedDecodeParams {
   PagedParams p;
@@ -53,16 +56,14 @@ template <int D>
 struct PagedDecodeCfg {
   static constexpr int kHalfBytes = kPdKeys * D * 2;  // K or V tile
   static constexpr int kStageBytes = 2 * kHalfBytes;
-  static constexpr int kStages = D == 128 ? 6 : 12;   // 192 KB in flight per SM
-  // A slot belongs to one set of warps for good: a set that met a slot only every other time could
-  // look at its barrier one phase too early (copies land in any order) and take the phase before
-  // last for its own.
-  static_assert(kStages % 2 == 0, "the sets take tiles, and with them slots, in turn");
+  static constexpr int kStages = D == 128 ? 3 : 6;    // 96 KB in flight per CTA
   static constexpr int kMergeFloats = kPdWarps / 2 * kPdRows * (D + 2);
   static constexpr int kBarOffset = kStages * kStageBytes + kMergeFloats * 4;
   static constexpr int kSegOffset = kBarOffset + (2 * kStages + 2 * kPdSegRing) * 8;
-  static constexpr int kSmemBytes = kSegOffset + kPdSegRing * 32 + 16 + 1024;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
+  static constexpr int kSumOffset = kSegOffset + kPdSegRing * 32 + 16;
+  static constexpr int kSmemBytes = kSumOffset + (kPdWarps + 1 + 2) * 8;
+  // two CTAs on an SM's 228 KB, of which 1 KB each is the system's
+  static_assert(kPdCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of two blocks");
 };
 
 __device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
@@ -70,9 +71,16 @@ __device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
   return static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.lens + b), 0)), cap));
 }
 
-// Tiles of sequence b on the line; an empty one takes a place as well (its rows are written).
-__device__ __forceinline__ int pd_tiles(const PagedParams& p, int b) {
-  return max(1, (paged_len(p, b) + kPdKeys - 1) / kPdKeys);
+// Tiles of an item over `len` keys; an empty one takes a place as well (its rows are written).
+__device__ __forceinline__ int pd_tiles(int len) { return max(1, (len + kPdKeys - 1) / kPdKeys); }
+
+// Length of an item of sequence b on the line.
+__device__ __forceinline__ int pd_cost(const PagedParams& p, int b) { return pd_tiles(paged_len(p, b)) + kPdItemCost; }
+
+// a / b of non-negative values, by the 32-bit division where both fit.
+__device__ __forceinline__ int64_t pd_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // Barrier of the consumer warps that also tells whether `pred` holds in any thread.
@@ -90,16 +98,15 @@ __device__ __forceinline__ bool pd_any(bool pred) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams a) {
+__global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedDecodeParams a) {
   using Cfg = PagedDecodeCfg<D>;
   constexpr int NS = Cfg::kStages;
   const PagedParams& p = a.p;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's pattern repeats every 1024 bytes
   const uint32_t ring = smem_u32(smem);
-  float* const s_o = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);  // [4 warps][16][D]
-  float* const s_m = s_o + kPdWarps / 2 * kPdRows * D;                        // [4][16]
-  float* const s_l = s_m + kPdWarps / 2 * kPdRows;                            // [4][16]
+  float* const s_o = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);  // [2 warps][16][D]
+  float* const s_m = s_o + kPdWarps / 2 * kPdRows * D;                        // [2][16]
+  float* const s_l = s_m + kPdWarps / 2 * kPdRows;                            // [2][16]
   const uint32_t bar0 = ring + Cfg::kBarOffset;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
@@ -109,16 +116,16 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
   // of the partial (-1: whole item)}
   volatile int* const segs = reinterpret_cast<volatile int*>(smem + Cfg::kSegOffset);
   volatile int* const abort_flag = segs + kPdSegRing * 8;
-  __shared__ int64_t s_sum[kPdThreads / 32];
-  __shared__ int64_t s_prefix;  // tiles of the sequences before this CTA's first one
-  __shared__ int s_first;       // that sequence
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + Cfg::kSumOffset);  // [5]
+  int64_t& s_prefix = s_sum[kPdWarps + 1];  // places of the sequences before this CTA's first one, per item
+  int64_t& s_first = s_sum[kPdWarps + 2];   // that sequence
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), kPdWarps / 2);
+      mbar_init(empty(s), kPdWarps);
     }
     for (int s = 0; s < kPdSegRing; ++s) {
       mbar_init(seg_full(s), 1);
@@ -139,47 +146,69 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 
   // ---- this CTA's share of the line
   const int per_seq = p.Hkv * a.row_groups;  // items per sequence
-  int64_t mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += kPdThreads) mine += pd_tiles(p, b);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-  if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kPdThreads / 32; ++w) total += s_sum[w];
-  total *= per_seq;
-  // every share has a tile at least; with fewer tiles than CTAs the last CTAs have none
   const int cta = static_cast<int>(blockIdx.x);
-  const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  const int64_t x0 = cta < G ? total * cta / G : 0;
-  const int64_t x1 = cta < G ? total * (cta + 1) / G : 0;
-  // the sequence that holds tile x0
-  int64_t base = 0;
-  for (int b0 = 0; b0 < p.B && x0 < x1; b0 += kPdThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    const int t = b < p.B ? pd_tiles(p, b) : 0;
-    int64_t incl = t;
+  int64_t total = 0, x0 = 0, x1 = 0;
+  int G = 0;
+  auto share = [&]() {
+    // every share has a place at least; with fewer places than CTAs the last CTAs have none
+    G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (cta < G) {
+      x0 = pd_div(total * cta, G);
+      x1 = pd_div(total * (cta + 1), G);
+    }
+  };
+  // Inclusive sum of t over the block's threads so far, and their total.
+  auto block_scan = [&](int t, int64_t& incl, int64_t& all) {
+    int w_incl = t;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += u;
+      const int u = __shfl_up_sync(0xffffffffu, w_incl, off);
+      if (lane >= off) w_incl += u;
     }
-    __syncthreads();  // s_sum's previous contents are read
-    if (lane == 31) s_sum[warp] = incl;
+    if (lane == 31) s_sum[warp] = w_incl;
     __syncthreads();
-    int64_t block = 0;
+    incl = w_incl;
+    all = 0;
 #pragma unroll
     for (int w = 0; w < kPdThreads / 32; ++w) {
       if (w < warp) incl += s_sum[w];
-      block += s_sum[w];
+      all += s_sum[w];
     }
-    if (t > 0 && (base + incl - t) * per_seq <= x0 && x0 < (base + incl) * per_seq) {
+  };
+  auto find = [&](int b, int t, int64_t end) {  // sequence b's places end at `end`
+    if (t > 0 && (end - t) * per_seq <= x0 && x0 < end * per_seq) {
       s_first = b;
-      s_prefix = base + incl - t;
+      s_prefix = end - t;
     }
-    base += block;
-    if (base * per_seq > x0) break;  // block-uniform
+  };
+  if (p.B <= kPdThreads) {
+    const int t = static_cast<int>(threadIdx.x) < p.B ? pd_cost(p, threadIdx.x) : 0;
+    int64_t incl;
+    block_scan(t, incl, total);
+    total *= per_seq;
+    share();
+    find(threadIdx.x, t, incl);
+  } else {
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += kPdThreads) mine += pd_cost(p, b);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPdThreads / 32; ++w) total += s_sum[w];
+    total *= per_seq;
+    share();
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B && x0 < x1 && base * per_seq <= x0; b0 += kPdThreads) {  // block-uniform
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      const int t = b < p.B ? pd_cost(p, b) : 0;
+      __syncthreads();  // s_sum's previous contents are read
+      int64_t incl, all;
+      block_scan(t, incl, all);
+      find(b, t, base + incl);
+      base += all;
+    }
   }
   __syncthreads();
 
@@ -211,12 +240,15 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
       ++nseg;
     };
     if (x0 < x1) {
-      int b = s_first;
+      int b = static_cast<int>(s_first);
       int L = paged_len(p, b);
-      int T = max(1, (L + kPdKeys - 1) / kPdKeys);
+      int T = pd_tiles(L);
       const int64_t in_seq = x0 - s_prefix * per_seq;
-      int hr = static_cast<int>(in_seq / T);
-      int tile = static_cast<int>(in_seq - static_cast<int64_t>(hr) * T);
+      int hr = static_cast<int>(pd_div(in_seq, T + kPdItemCost));
+      // places of the share that lie before the item's end: an item's first kPdItemCost places stand
+      // for its fixed cost, the others for its tiles
+      int64_t xs = s_prefix * per_seq + static_cast<int64_t>(hr) * (T + kPdItemCost);
+      int tile = max(0, static_cast<int>(x0 - xs) - kPdItemCost);
       // the page of this lane's copy of tile `tl`: a table entry, oob_page when it is none, -1 behind the last key
       auto page_of = [&](int bb, int tl, int len) -> int {
         const int key = tl * kPdKeys + (box << pb_shift);
@@ -229,33 +261,45 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         return page;
       };
       int page = page_of(b, tile, L);
-      int64_t x = x0;
-      while (ok && x < x1) {
+      while (ok && xs + kPdItemCost < x1) {
         // a piece: tiles tile .. of item (b, hr), to its end or the share's
-        const int n = static_cast<int>(min(static_cast<int64_t>(T - tile), x1 - x));
+        const int n = static_cast<int>(min(static_cast<int64_t>(T), x1 - xs - kPdItemCost)) - tile;
         const bool whole = tile == 0 && n == T;
+        const int head = hr / a.row_groups;
+        {
+          // the piece's query rows into the first-level cache (rows of a token are contiguous)
+          const int r0 = (hr - head * a.row_groups) * kPdRows;
+          const int lines = D * 2 / 128;
+          const int r = r0 + lane / lines;
+          if (lane < kPdRows * lines && r < p.group * p.Sq) {
+            const int i = r / p.group;
+            prefetch_l1(p.q + ((static_cast<int64_t>(b) * p.Sq + i) * p.Hq + head * p.group + r - i * p.group) * D +
+                        (lane % lines) * 64);
+          }
+        }
         if (tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != L) atomicOr(&g_error_word, kErrSeqlen);
         if (tile == 0 && n < T) {
-          const int64_t last = x + T - 1;  // the item's last tile, and the CTA whose share holds it
-          join = make_int4(b, hr, static_cast<int>(((last + 1) * G - 1) / total), 0);
+          const int64_t last = xs + kPdItemCost + T;  // the CTA whose share holds the item's last tile
+          join = make_int4(b, hr, static_cast<int>(pd_div(last * G - 1, total)), 0);
         }
         const int nk = L > 0 ? n : 0;
         announce(b, hr, tile, nk, L, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
-        const int head = hr / a.row_groups;
-        int nb2 = b, nhr = hr + 1, nL = L, nT = T;  // the item behind this one
+        const int64_t xe = xs + kPdItemCost + T;
+        const bool more = xe + kPdItemCost < x1;  // the next item has tiles in this share
+        int nb2 = b, nhr = hr + 1, nL = L, nT = T;
         if (nhr == per_seq) {
           nhr = 0;
           nb2 = b + 1;
-          if (x + n < x1) {
+          if (more) {
             nL = paged_len(p, nb2);
-            nT = max(1, (nL + kPdKeys - 1) / kPdKeys);
+            nT = pd_tiles(nL);
           }
         }
         for (int i = 0; ok && i < nk; ++i) {
           const int tl = tile + i;
           const int cur = page;
           if (i + 1 < nk) page = page_of(b, tl + 1, L);
-          else if (x + n < x1) page = page_of(nb2, 0, nL);
+          else if (more) page = page_of(nb2, 0, nL);
           const int st = issued % NS;
           ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((issued / NS) & 1) ^ 1, abort_flag));
           if (!ok) break;
@@ -269,8 +313,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
           }
           ++issued;
         }
-        if (nk == 0 && x + n < x1) page = page_of(nb2, 0, nL);
-        x += n;
+        if (nk == 0 && more) page = page_of(nb2, 0, nL);
+        xs = xe;
         b = nb2;
         hr = nhr;
         L = nL;
@@ -289,8 +333,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 
   // ------------------------------------------------------------ consumers
   const float c = p.scale_log2;
-  const int set = warp >> 2;           // which of every two tiles
-  const int kb = (warp & 3) * 16;      // this warp's 16 keys of a tile
+  const int kb = warp * 16;            // this warp's 16 keys of a tile
   const int qr = lane >> 2;            // fragment row (and row + 8)
   const int qc = (lane & 3) * 2;       // fragment column pair
   const int rows_total = p.group * p.Sq;
@@ -313,7 +356,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
   for (int sg = 0;; ++sg) {
     const int sk = sg % kPdSegRing;
     bool ok = __all_sync(0xffffffffu, mbar_wait(seg_full(sk), (sg / kPdSegRing) & 1, abort_flag));
-    int b = -1, hr = 0, tile0 = 0, n = 0, L = 0, slot = 0;
+    int b = -1, hr = 0, tile0 = 0, n = 0, L = 0;
     if (ok) {
       volatile int* s = segs + 8 * sk;
       b = s[0];
@@ -321,12 +364,9 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
       tile0 = s[2];
       n = s[3];
       L = s[4];
-      slot = s[5];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(seg_empty(sk));
     }
-    const int head = hr / a.row_groups;
-    const int row0 = (hr - head * a.row_groups) * kPdRows;  // first of the head's query rows
+    int head = hr / a.row_groups;
+    int row0 = (hr - head * a.row_groups) * kPdRows;  // first of the head's query rows
     const int rows = min(kPdRows, rows_total - row0);
     float o[D / 8][4];
 #pragma unroll
@@ -353,8 +393,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
           qf[ks][2 + h] = live ? __ldg(q + ((ks * 16 + 8 + qc) >> 1)) : 0u;
         }
       }
-      // tile number it of the CTA goes to set it mod 2
-      for (int i = (it0 ^ set) & 1; i < n; i += 2) {
+      for (int i = 0; i < n; ++i) {
         const int it = it0 + i;
         const int st = it % NS;
         if (!__all_sync(0xffffffffu, mbar_wait(full(st), (it / NS) & 1, abort_flag))) {
@@ -406,12 +445,15 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             pa[2] = pack_bf16x2(p10, p11);
             pa[3] = pack_bf16x2(p12, p13);
           }
+          // most tiles leave every maximum where it was
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-          for (int e = 0; e < D / 8; ++e) {
-            o[e][0] *= alpha[0];
-            o[e][1] *= alpha[0];
-            o[e][2] *= alpha[1];
-            o[e][3] *= alpha[1];
+            for (int e = 0; e < D / 8; ++e) {
+              o[e][0] *= alpha[0];
+              o[e][1] *= alpha[0];
+              o[e][2] *= alpha[1];
+              o[e][3] *= alpha[1];
+            }
           }
           // Rows of V behind the last key hold whatever the page holds, and 0
           // times infinity or NaN is NaN: those keys' values are zeroed.  A
@@ -447,9 +489,13 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       }
     }
-    // ---- merge of the eight warps: the second set leaves its rows in shared
-    // memory, the first adds them to its own and leaves the sums there.
-    const int mw = warp & 3;
+    // ---- merge of the four warps: the upper two leave their rows in shared
+    // memory, the lower two add them to their own and leave the sums there.  A
+    // row's columns are exchanged by eights so that four rows fill the 32 banks.
+    const int mw = warp & 1;
+    int x = qr;
+    asm volatile("" : "+r"(x));  // the offsets below are not to be held in registers over the tiles
+    const uint32_t part = smem_u32(s_o) + ((mw * kPdRows + x) * D + qc) * 4;  // row qr's column qc of eight 0
     auto leave = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -457,8 +503,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         if (r < rows) {
 #pragma unroll
           for (int e = 0; e < D / 8; ++e)
-            *reinterpret_cast<float2*>(&s_o[(mw * kPdRows + r) * D + e * 8 + qc]) =
-                make_float2(o[e][2 * h], o[e][2 * h + 1]);
+            st_shared_f2(part + h * (8 * D * 4) + (e & ~3) * 32 + (((e ^ x) & 3) << 5), o[e][2 * h], o[e][2 * h + 1]);
           if ((lane & 3) == 0) {
             s_m[mw * kPdRows + r] = m[h];
             s_l[mw * kPdRows + r] = l[h];
@@ -466,10 +511,10 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
       }
     };
-    if (n > 0 && set == 1) leave();
+    if (n > 0 && warp >= 2) leave();
     // every consumer meets here once per piece, and all of them leave together
     if (pd_any(!ok) || b < 0) break;
-    if (n > 0 && set == 0) {
+    if (n > 0 && warp < 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = qr + 8 * h;
@@ -482,9 +527,9 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
           l[h] = l[h] * w0 + l1 * w1;
 #pragma unroll
           for (int e = 0; e < D / 8; ++e) {
-            const float2 x = *reinterpret_cast<const float2*>(&s_o[(mw * kPdRows + r) * D + e * 8 + qc]);
-            o[e][2 * h] = o[e][2 * h] * w0 + x.x * w1;
-            o[e][2 * h + 1] = o[e][2 * h + 1] * w0 + x.y * w1;
+            const float2 y = ld_shared_f2(part + h * (8 * D * 4) + (e & ~3) * 32 + (((e ^ x) & 3) << 5));
+            o[e][2 * h] = o[e][2 * h] * w0 + y.x * w1;
+            o[e][2 * h + 1] = o[e][2 * h + 1] * w0 + y.y * w1;
           }
         }
       }
@@ -492,11 +537,19 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
       leave();
     }
     named_bar_sync(1, kPdWarps * 32);
-    // 16 threads per row, D/16 consecutive columns each
-    const int r = static_cast<int>(threadIdx.x) >> 4;
+    // the announced piece again: it need not stay in registers over the tiles
+    b = segs[8 * sk];
+    hr = segs[8 * sk + 1];
+    const int slot = segs[8 * sk + 5];
+    head = hr / a.row_groups;
+    row0 = (hr - head * a.row_groups) * kPdRows;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(sk));
+    // 8 threads per row, D/8 consecutive columns each
+    const int r = static_cast<int>(threadIdx.x) >> 3;
     if (r < rows) {
-      constexpr int kCols = D / 16;
-      const int c0 = (static_cast<int>(threadIdx.x) & 15) * kCols;
+      constexpr int kCols = D / 8;
+      const int c0 = (static_cast<int>(threadIdx.x) & 7) * kCols;
       float M = -INFINITY, sum = 0.f;
       float wt[kPdWarps / 2];
       float acc[kCols];
@@ -516,7 +569,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         for (int w = 0; w < kPdWarps / 2; ++w)
 #pragma unroll
           for (int e = 0; e < kCols; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * kPdRows + r) * D + c0 + e]);
+            const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * kPdRows + r) * D + ((c0 + e) ^ ((r & 3) * 8))]);
             acc[e] += wt[w] * v.x;
             acc[e + 1] += wt[w] * v.y;
             acc[e + 2] += wt[w] * v.z;
@@ -550,28 +603,46 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 
 // Join the partial rows of the items that cross shares: block c takes the item
 // that begins in CTA c's share, one warp per row.  With w_s = l_s exp(m_s - M),
-// M = max_s m_s: o = sum_s w_s o_s / sum_s w_s, lse = M + ln sum_s w_s.
+// M = max_s m_s: o = sum_s w_s o_s / sum_s w_s, lse = M + ln sum_s w_s.  All that
+// an item of up to kJoinRows pieces needs is loaded at once, before it is known
+// which pieces there are (what is read beyond them is not used): one memory
+// latency, not one per step.
+constexpr int kJoinRows = 8;
+
 template <int D>
 __global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const __grid_constant__ PagedDecodeParams a) {
   constexpr int kPer = D / 32;
   constexpr float kLog2e = 1.4426950408889634f;
   const PagedParams& p = a.p;
   grid_dependency_trigger();
-  grid_dependency_wait();
-  const int cta = static_cast<int>(blockIdx.x);
-  const int4 join = a.joins[cta];
+  const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
   const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // piece 0 lies in CTA cta's slot for the item it begins, piece s in CTA cta + s's for the one it continues
+  auto slot_row = [&](int s) { return (2 * min(cta + s, ctas - 1) + (s == 0 ? 1 : 0)) * kPdRows + r; };
+  auto load = [&](int s, float (&x)[kPer]) {
+    const float* src = a.part_o + static_cast<int64_t>(slot_row(s)) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const float2 t = *reinterpret_cast<const float2*>(src + e);
+      x[e] = t.x;
+      x[e + 1] = t.y;
+    }
+  };
+  grid_dependency_wait();
+  const int4 join = a.joins[cta];
+  float2 ml = a.part_ml[slot_row(lane)];
+  float x[kJoinRows][kPer];
+#pragma unroll
+  for (int u = 0; u < kJoinRows; ++u) load(u, x[u]);
   if (join.x < 0) return;
   const int head = join.y / a.row_groups;
   const int row = (join.y - head * a.row_groups) * kPdRows + r;  // of the head's query rows
   if (row >= p.group * p.Sq) return;
   const int pieces = join.z - cta + 1;
-  // piece 0 lies in CTA cta's slot for the item it begins, piece s in CTA cta + s's for the one it continues
-  auto slot_row = [&](int s) { return static_cast<int64_t>(2 * (cta + s) + (s == 0 ? 1 : 0)) * kPdRows + r; };
   float M = -INFINITY;
-  for (int s = lane; s < pieces; s += 32) {
-    const float2 v = a.part_ml[slot_row(s)];
-    if (v.y > 0.f) M = fmaxf(M, v.x);
+  for (int s0 = 0; s0 < pieces; s0 += 32) {
+    const float2 v = s0 == 0 ? ml : a.part_ml[slot_row(s0 + lane)];
+    if (s0 + lane < pieces && v.y > 0.f) M = fmaxf(M, v.x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -580,17 +651,24 @@ __global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const _
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   float W = 0.f;
   if (M != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < pieces; ++s) {
-      const float2 v = a.part_ml[slot_row(s)];
-      const float w = v.y > 0.f ? v.y * ex2_approx((v.x - M) * kLog2e) : 0.f;
-      W += w;
-      const float* src = a.part_o + slot_row(s) * D + lane * kPer;
+    float w_lane = 0.f;
+    for (int s0 = 0; s0 < pieces; s0 += kJoinRows) {
+      if ((s0 & 31) == 0) {
+        if (s0 > 0) ml = a.part_ml[slot_row(s0 + lane)];
+        w_lane = s0 + lane < pieces && ml.y > 0.f ? ml.y * ex2_approx((ml.x - M) * kLog2e) : 0.f;
+      }
+      if (s0 > 0) {
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + e);
-        acc[e] = fmaf(w, x.x, acc[e]);
-        acc[e + 1] = fmaf(w, x.y, acc[e + 1]);
+        for (int u = 0; u < kJoinRows; ++u) load(s0 + u, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinRows; ++u) {
+        const float w = __shfl_sync(0xffffffffu, w_lane, (s0 + u) & 31);
+        if (s0 + u < pieces) {
+          W += w;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
+        }
       }
     }
   }

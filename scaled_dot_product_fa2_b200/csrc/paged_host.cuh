@@ -101,7 +101,7 @@ bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int
 
 // The decode's workspace: two partial row sets and one join per CTA of the grid.
 size_t paged_decode_ws_bytes(int sms, int d) {
-  return static_cast<size_t>(sms) * (2 * kPdRows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
+  return static_cast<size_t>(kPdCtasPerSm * sms) * (2 * kPdRows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
                                      sizeof(int4));
 }
 
@@ -117,7 +117,7 @@ attn_status_t launch_paged_decode(const PagedDecodeParams& a, int sms, int dev, 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(kPdCtasPerSm * sms));
   cfg.blockDim = dim3(kPdThreads);
   cfg.dynamicSmemBytes = PagedDecodeCfg<D>::kSmemBytes;
   cfg.stream = st;
@@ -301,8 +301,8 @@ attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t*
       !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box))
     return ATTN_ERR_CUDA;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * sms) * kPdRows * d);
-  a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(2 * sms) * kPdRows);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows * d);
+  a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d == 128 ? launch_paged_decode<128>(a, sms, dev, st) : launch_paged_decode<64>(a, sms, dev, st);
 }
