@@ -2,8 +2,8 @@
 
 Usage: ``python -m scaled_dot_product_fa2_b200.build [--force]``.  The build
 also checks ptxas' report: no kernel may spill registers, and the prefill
-kernels must launch at exactly the register count their in-kernel setmaxnreg
-split is written for.
+kernels (the paged forward among them) must launch at exactly the register
+count their in-kernel setmaxnreg split is written for.
 """
 from __future__ import annotations
 
@@ -63,7 +63,7 @@ def check_ptxas_report(report: str) -> None:
             if int(m.group(1)) > allowed or int(m.group(2)) > allowed:
                 raise RuntimeError(f"kernel {current} spills registers:\n{line}")
         m = re.search(r"Used (\d+) registers", line)
-        if m and current and "prefill_kernel" in current and int(m.group(1)) != PREFILL_LAUNCH_REGS:
+        if m and current and ("prefill_kernel" in current or "paged_fwd_kernel" in current) and int(m.group(1)) != PREFILL_LAUNCH_REGS:
             raise RuntimeError(f"{current} uses {m.group(1)} registers, expected {PREFILL_LAUNCH_REGS}")
 
 

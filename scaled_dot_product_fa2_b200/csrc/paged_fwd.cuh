@@ -1,0 +1,908 @@
+// paged_fwd.cuh -- attention of ragged chunks of new tokens over a paged KV
+// cache, on tcgen05 (see paged.cuh for the formula).
+//
+// Long chunks are bound by the tensor cores and single tokens by the bytes of
+// their cache; both come in one batch, so one kernel serves both, built like
+// the forward of prefill.cuh (same roles, barriers and softmax; the comments
+// there hold here) with these differences:
+//   * A query tile packs the query heads of one KV head: row r of 128 is token
+//     r / hc, head r mod hc of the hc <= 128 heads (all of the group where it
+//     fits).  K/V are loaded once for the whole group, and a chunk of n tokens
+//     fills its tiles with n * hc rows: 32 tokens of 4 heads are a full tile.
+//   * A unit is two such tiles that share every K/V tile.  A unit with rows in
+//     one tile only (a single token, a chunk's end) is thin: both tiles hold
+//     the same rows and take key tiles in turn, so the two softmax chains still
+//     overlap, and the unit's two results are merged in the epilogue (the
+//     second one's output is read from its own TMEM columns).
+//   * All units' keys form one line, in the order (sequence, KV head, unit), cut
+//     into equal shares, one per CTA (one CTA per SM); a share may begin and end
+//     inside a unit.  A pair's key weighs 2, a thin unit's 1, and a unit has a
+//     fixed weight besides.  A unit's visible keys are linear in its index, so
+//     sums over a sequence's units are closed forms and every CTA finds its
+//     place from the lengths on the device.  A unit that crosses shares leaves
+//     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
+//     programmatic dependent, joins in share order.
+//   * K/V tiles of 128 keys arrive as one TMA copy per page (or 128 rows of it)
+//     and 64 columns; the producer's lanes issue them side by side, each with
+//     the table entry it read one tile ahead.  Keys behind the last page read as
+//     zeros (a page index behind the map's end).  The last page's rows behind
+//     the last key hold anything, and 0 times infinity or NaN is NaN, so warp 11
+//     zeroes them in V's last tile before the MMAs may read it.
+#pragma once
+#include "paged.cuh"
+#include "prefill.cuh"
+
+namespace sdpa {
+
+constexpr int kPfUnitCost = 512;   // a unit's fixed weight (two pair steps' worth of keys: measured boundary)
+constexpr int kPfRing = 4;         // pieces announced ahead
+constexpr int kPfTailWarp = 11;
+
+struct PagedFwdParams {
+  PagedParams p;
+  CUtensorMap tm_q;   // 4-D (d, head in group, KV head, token), box {64, hc, 1, tpt}, 128-byte swizzle
+  CUtensorMap tm_k;   // 5-D (64 columns, page row, column block, head, page), box {64, min(P, 128), 1, 1, 1}
+  CUtensorMap tm_v;
+  int oob_page;       // a page index behind the map's last one (reads as zeros)
+  int hc, chunks;     // heads per tile, tiles of heads per group
+  int tpt;            // tokens per tile: 128 / hc
+  FastDiv div_hc;
+  float* part_o;      // [2 * CTAs][2 tiles][d][128 rows] locally normalised partial outputs
+  float2* part_ml;    // [2 * CTAs][2 tiles][128] (max of scale * q.k, sum)
+  int4* joins;        // [CTAs][2] {first token, first head, heads, last CTA (-1: no join)}, {tokens of tile 0, 1, -, -}
+};
+
+template <int D, int NS>
+struct PagedFwdCfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kBlockBytes = 128 * 128;
+  // q_full[2] q_empty[2] kv_full[NS] kv_empty[NS] s_full[2] p_full[2] o_full[2] turn[2] drain
+  // unit_full[4] unit_empty[4] merge_full merge_done tail[NS]
+  static constexpr int kNumBars = 4 + 2 * NS + 8 + 1 + 2 * kPfRing + 2 + NS;
+  static constexpr int kRingOffset = (kNumBars * 8 + 15) / 16 * 16;   // pieces: kPfRing x 16 ints
+  static constexpr int kMergeOffset = kRingOffset + kPfRing * 64;     // thin units: (max, sum) of tile 1's rows
+  static constexpr int kSumOffset = kMergeOffset + 128 * 8;           // 12 sums, prefix, first sequence
+  static constexpr int kMiscOffset = kSumOffset + 14 * 8;             // TMEM base, abort flag
+  static constexpr int kSmemBytes = (2 + NS) * kTileBytes + kMiscOffset + 8;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
+};
+
+// A sequence's place in the batch.
+struct PfSeq {
+  int start, n;     // first token, tokens
+  int L, coff;      // keys; token i sees key j iff j <= i + coff (causal)
+  int full, units;  // units whose two tiles are full, units
+  int64_t cost;     // weight of its units for one (KV head, head tile)
+};
+
+__device__ __forceinline__ int pf_visible(int causal, int64_t tokens, int L, int coff) {
+  return causal ? static_cast<int>(min(max(tokens + coff, int64_t{0}), static_cast<int64_t>(L))) : L;
+}
+
+// Weight of the first V full units (tu tokens each): V times the fixed weight
+// and twice the visible keys, which are clamp((v + 1) tu + coff, 0, L) in unit v.
+__device__ __forceinline__ int64_t pf_prefix(int causal, int V, int tu, int L, int coff) {
+  const int64_t fixed = static_cast<int64_t>(V) * kPfUnitCost;
+  if (!causal) return fixed + 2 * static_cast<int64_t>(V) * L;
+  const int lo = min(V, max(-coff, 0) / tu);                     // units that see nothing
+  const int hi = min(V, max(lo, (L - coff + tu - 1) / tu - 1));  // first unit that sees every key
+  const int64_t m = hi - lo;
+  const int64_t mid = m * coff + tu * (static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2;
+  return fixed + 2 * (mid + static_cast<int64_t>(V - hi) * L);
+}
+
+__device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b, bool report) {
+  const PagedParams& p = a.p;
+  PfSeq s;
+  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), raw = __ldg(p.lens + b);
+  s.start = min(max(c0, 0), p.T);
+  const int end = min(max(c1, s.start), p.T);
+  s.n = end - s.start;
+  s.L = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), static_cast<int64_t>(p.max_pages) << p.page_shift));
+  if (report && (s.start != c0 || end != c1 || s.L != raw)) atomicOr(&g_error_word, kErrSeqlen);
+  s.coff = p.causal == 2 ? s.L - s.n : 0;
+  const int tu = 2 * a.tpt;
+  s.full = s.n / tu;
+  const int rem = s.n - s.full * tu;
+  s.units = s.full + (rem > 0 ? 1 : 0);
+  s.cost = pf_prefix(p.causal, s.full, tu, s.L, s.coff);
+  if (rem > 0) s.cost += kPfUnitCost + (rem > a.tpt ? 2 : 1) * static_cast<int64_t>(pf_visible(p.causal, s.n, s.L, s.coff));
+  return s;
+}
+
+template <int D, int NS>
+__global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __grid_constant__ PagedFwdParams a) {
+  using Cfg = PagedFwdCfg<D, NS>;
+  const PagedParams& p = a.p;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's pattern repeats every 1024 bytes
+  const uint32_t sQ = smem_u32(smem);
+  const uint32_t sKV = sQ + 2 * Cfg::kTileBytes;
+  const uint32_t bar0 = sKV + NS * Cfg::kTileBytes;
+  auto q_full = [&](int t) { return bar0 + 8u * t; };
+  auto q_empty = [&](int t) { return bar0 + 8u * (2 + t); };
+  auto kv_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + NS + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (4 + 2 * NS + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (6 + 2 * NS + t); };
+  auto o_full = [&](int t) { return bar0 + 8u * (8 + 2 * NS + t); };
+  auto turn = [&](int t) { return bar0 + 8u * (10 + 2 * NS + t); };
+  const uint32_t drain = bar0 + 8u * (12 + 2 * NS);
+  auto unit_full = [&](int k) { return bar0 + 8u * (13 + 2 * NS + k); };
+  auto unit_empty = [&](int k) { return bar0 + 8u * (13 + 2 * NS + kPfRing + k); };
+  const uint32_t merge_full = bar0 + 8u * (13 + 2 * NS + 2 * kPfRing);  // thin unit: tile 1's result is complete
+  const uint32_t merge_done = merge_full + 8;                           // thin unit: it was read
+  // a V tile that warp 11 has to clean landed in the slot; one barrier per slot, because a slot is not
+  // filled again before it was cleaned (one for all could run two phases ahead of the cleaner)
+  auto tail = [&](int s) { return merge_full + 16 + 8u * s; };
+  uint8_t* const misc = smem + (2 + NS) * Cfg::kTileBytes;
+  volatile int* const ring = reinterpret_cast<volatile int*>(misc + Cfg::kRingOffset);
+  float2* const merge_ml = reinterpret_cast<float2*>(misc + Cfg::kMergeOffset);
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(misc + Cfg::kSumOffset);
+  int64_t& s_prefix = s_sum[12];  // weight of the sequences before this CTA's first one, per (KV head, head tile)
+  int64_t& s_first = s_sum[13];   // that sequence
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + Cfg::kMiscOffset);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // Entries of an announced piece.
+  enum { kHead, kG0, kHeads, kTok0, kCnt0, kCnt1, kLim, kKeys, kJ0, kN0, kN1, kThin, kSlot, kSteps };
+  // The r-th piece of this CTA: waits for it; nullptr where there is none left.
+  // The caller's whole warp (or its lone thread) calls it and releases it with
+  // `release` when it has read what it needs.
+  auto next_piece = [&](int r, bool& ok) -> volatile int* {
+    const int k = r % kPfRing;
+    ok = ok && mbar_wait(unit_full(k), (r / kPfRing) & 1, abort_flag);
+    volatile int* const e = ring + 16 * k;
+    return ok && e[kHead] >= 0 ? e : nullptr;
+  };
+  auto release = [&](int r) {
+    __syncwarp(__activemask());
+    if ((threadIdx.x & 31) == 0 || __activemask() == 1u) mbar_arrive(unit_empty(r % kPfRing));
+  };
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(turn(t), 1);
+      mbar_init(o_full(t), 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 2);
+      mbar_init(tail(s), 1);
+    }
+    mbar_init(drain, 2);
+    for (int k = 0; k < kPfRing; ++k) {
+      mbar_init(unit_full(k), 1);
+      mbar_init(unit_empty(k), 2 + 8 + 1);  // MMA threads, softmax warps, tail warp
+    }
+    mbar_init(merge_full, 4);
+    mbar_init(merge_done, 4);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Launched as a programmatic dependent of whatever precedes it on the stream:
+  // no global memory is touched before this wait.
+  grid_dependency_wait();
+  grid_dependency_trigger();
+
+  // ---- this CTA's share of the line
+  const int cta = static_cast<int>(blockIdx.x);
+  const int per_seq = p.Hkv * a.chunks;
+  int64_t x0 = 0, x1 = 0, total = 0;
+  int G = 0;
+  {
+    constexpr int kWarps = kPrefillThreads / 32;
+    auto cost_of = [&](int b) -> int64_t { return b < p.B ? pf_seq(a, b, cta == 0).cost : 0; };
+    // inclusive sum over the block's threads and their total
+    auto block_scan = [&](int64_t t, int64_t& incl, int64_t& all) {
+      incl = t;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += u;
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += s_sum[w];
+        all += s_sum[w];
+      }
+    };
+    auto share = [&]() {
+      // a share is at least a pair step long (256), so each CTA between the first and the last one of
+      // a unit has a key tile of it
+      G = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), total / 256)));
+      if (cta < G) {
+        x0 = total / G * cta + total % G * cta / G;
+        x1 = total / G * (cta + 1) + total % G * (cta + 1) / G;
+      }
+    };
+    auto find = [&](int b, int64_t t, int64_t end) {  // sequence b's weights end at `end`
+      if (t > 0 && (end - t) * per_seq <= x0 && x0 < end * per_seq) {
+        s_first = b;
+        s_prefix = end - t;
+      }
+    };
+    if (p.B <= kPrefillThreads) {
+      const int64_t t = cost_of(threadIdx.x);
+      int64_t incl;
+      block_scan(t, incl, total);
+      total *= per_seq;
+      share();
+      find(threadIdx.x, t, incl);
+    } else {
+      int64_t mine = 0, incl, all;
+      for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) mine += cost_of(b);
+      block_scan(mine, incl, total);
+      total *= per_seq;
+      share();
+      int64_t base = 0;
+      for (int b0 = 0; b0 < p.B && x0 < x1 && base * per_seq <= x0; b0 += kPrefillThreads) {  // block-uniform
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        const int64_t t = cost_of(b);
+        __syncthreads();  // s_sum's previous contents are read
+        block_scan(t, incl, all);
+        find(b, t, base + incl);
+        base += all;
+      }
+    }
+    __syncthreads();
+  }
+
+  if (warp >= 8) {
+    regs_decrease<kCtrlRegs>();
+    if (warp == kLoadWarp) {
+      // ------------------------------------------- producer and scheduler
+      const int pb_shift = min(p.page_shift, 7);
+      const int pb = 1 << pb_shift;         // rows per copy
+      const int nb = 128 >> pb_shift;       // copies per 64 columns of a tile
+      const int blk = lane / nb, box = lane - blk * nb;
+      const bool copier = blk < Cfg::kBlocks;
+      const uint32_t box_dst = static_cast<uint32_t>(blk) * Cfg::kBlockBytes + static_cast<uint32_t>(box) * pb * 128u;
+      const int tu = 2 * a.tpt;
+      const uint32_t q_bytes = static_cast<uint32_t>(a.hc) * a.tpt * D * 2;
+      int it = 0;    // K/V tiles issued so far
+      int ui = 0;    // pieces started so far
+      uint32_t tail_uses = 0;    // per slot: parity of the tiles handed to warp 11
+      uint32_t slot_tail = 0;    // per slot: its last tile was one of them
+      bool ok = true;
+      int4 join0 = make_int4(0, 0, 0, -1), join1 = make_int4(0, 0, 0, 0);
+      auto page_of = [&](int b, int j, int L) -> int {  // the page of this lane's copy of key tile j
+        const int key = j * 128 + box * pb;
+        if (!copier || key >= L) return a.oob_page;
+        int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift));
+        if (page < 0 || page >= p.num_pages) {
+          atomicOr(&g_error_word, kErrPage);
+          page = a.oob_page;
+        }
+        return page;
+      };
+      if (x0 < x1) {
+        int b = static_cast<int>(s_first);
+        PfSeq s = pf_seq(a, b, false);
+        const int64_t in_seq = x0 - s_prefix * per_seq;
+        int hr = static_cast<int>(in_seq / s.cost);   // KV head * chunks + head tile
+        const int64_t in_head = in_seq - hr * s.cost;
+        int v = 0;
+        for (int hi = s.units; hi - v > 1;) {  // last unit that begins at or before the share
+          const int mid = (v + hi) >> 1;
+          if (pf_prefix(p.causal, mid, tu, s.L, s.coff) <= in_head) v = mid;
+          else hi = mid;
+        }
+        int64_t xs = x0 - in_head + pf_prefix(p.causal, v, tu, s.L, s.coff);  // where the unit begins
+        while (ok && xs < x1) {
+          // unit (b, hr, v): tokens v tu .. of the sequence
+          const int cnt0 = min(s.n - v * tu, a.tpt);
+          const int cnt1 = min(max(s.n - v * tu - a.tpt, 0), a.tpt);
+          const bool thin = cnt1 == 0;
+          const int w = thin ? 1 : 2;
+          const int64_t t0 = static_cast<int64_t>(v) * tu;
+          const int keys = pf_visible(p.causal, t0 + cnt0 + cnt1, s.L, s.coff);
+          const int n_u = (keys + 127) / 128;                                          // its key tiles
+          const int n_0 = (pf_visible(p.causal, t0 + cnt0, s.L, s.coff) + 127) / 128;  // tile 0's
+          // key tile k stands at xs + kPfUnitCost + 128 w k
+          auto tile_at = [&](int64_t x) -> int {
+            const int64_t off = x - xs - kPfUnitCost;
+            return off <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(n_u), (off + 128 * w - 1) / (128 * w)));
+          };
+          const int j0 = tile_at(x0), j1 = tile_at(x1);
+          const int64_t xe = xs + kPfUnitCost + static_cast<int64_t>(w) * keys;
+          if (j1 > j0 || (n_u == 0 && xs >= x0)) {
+            const int steps = j1 - j0;
+            const bool whole = steps == n_u;
+            const int hk = hr / a.chunks, chunk = hr - hk * a.chunks;
+            const int g0 = chunk * a.hc;
+            const int heads = min(a.hc, p.group - g0);
+            const int tok0 = s.start + static_cast<int>(t0);
+            int n0, n1;
+            if (thin) {
+              n0 = (steps + 1) >> 1;
+              n1 = steps >> 1;
+            } else {
+              n0 = min(max(n_0 - j0, 0), steps);
+              n1 = steps;
+            }
+            if (j0 == 0 && !whole) {
+              const int64_t last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * 128 * w;
+              // the CTA whose share holds the unit's last key tile
+              int c = static_cast<int>(last / (total / G + 1));  // at most the right one
+              while (c + 1 < G && total / G * (c + 1) + total % G * (c + 1) / G <= last) ++c;
+              join0 = make_int4(tok0, hk * p.group + g0, heads, c);
+              join1 = make_int4(cnt0, cnt1, 0, 0);
+            }
+            // announce
+            const int k = ui % kPfRing;
+            ok = __all_sync(0xffffffffu,
+                            ui < kPfRing || mbar_wait(unit_empty(k), ((ui / kPfRing) - 1) & 1, abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+              volatile int* e = ring + 16 * k;
+              e[kHead] = hk;
+              e[kG0] = hk * p.group + g0;
+              e[kHeads] = heads;
+              e[kTok0] = tok0;
+              e[kCnt0] = cnt0;
+              e[kCnt1] = cnt1;
+              e[kLim] = static_cast<int>(t0) + s.coff;
+              e[kKeys] = s.L;
+              e[kJ0] = j0;
+              e[kN0] = n0;
+              e[kN1] = n1;
+              e[kThin] = thin;
+              e[kSlot] = whole ? -1 : (j0 > 0 ? 2 * cta : 2 * cta + 1);
+              e[kSteps] = steps;
+              mbar_arrive(unit_full(k));
+            }
+            __syncwarp();
+            // Q_0, Q_1: each once the previous piece's last S MMA on that buffer is done
+            auto load_q = [&]() -> bool {
+              for (int t = 0; t < 2; ++t) {
+                if (ui > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty(t), (ui - 1) & 1, abort_flag))) return false;
+                if (lane == 0) {
+                  if ((t ? n1 : n0) > 0) {
+                    mbar_arrive_expect_tx(q_full(t), q_bytes);
+                    for (int c = 0; c < Cfg::kBlocks; ++c)
+                      tma_load_4d(sQ + t * Cfg::kTileBytes + c * Cfg::kBlockBytes, &a.tm_q, c * 64, g0, hk,
+                                  tok0 + (thin ? 0 : t * a.tpt), q_full(t));
+                  } else {
+                    mbar_arrive(q_full(t));
+                  }
+                }
+                __syncwarp();
+              }
+              return true;
+            };
+            if (steps <= 1) ok = load_q();
+            int page = page_of(b, j0, s.L);
+#pragma unroll 1
+            for (int x = 0; ok && x < steps; ++x) {
+              const int j = j0 + x;
+              if (x == 1 && !load_q()) {  // after K_0, V_0
+                ok = false;
+                break;
+              }
+              const int cur = page;
+              if (x + 1 < steps) page = page_of(b, j + 1, s.L);
+              const int row = (j * 128 + box * pb) & ((1 << p.page_shift) - 1);
+              const bool clean = (j + 1) * 128 > s.L;  // V's rows behind the last key
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv, ++it) {
+                const int slot = it % NS;
+                if (!__all_sync(0xffffffffu, mbar_wait(kv_empty(slot), ((it / NS) & 1) ^ 1, abort_flag))) {
+                  ok = false;
+                  break;
+                }
+                const bool to_clean = kv && clean;
+                const uint32_t bar = to_clean ? tail(slot) : kv_full(slot);
+                tail_uses ^= (to_clean ? 1u : 0u) << slot;
+                slot_tail = (slot_tail & ~(1u << slot)) | ((to_clean ? 1u : 0u) << slot);
+                if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+                __syncwarp();
+                if (copier)
+                  tma_load_5d(sKV + slot * Cfg::kTileBytes + box_dst, kv ? &a.tm_v : &a.tm_k, 0, row, blk, hk, cur, bar);
+              }
+            }
+            ++ui;
+          }
+          // the unit behind this one
+          xs = xe;
+          if (++v == s.units) {
+            v = 0;
+            if (++hr == per_seq) {
+              hr = 0;
+              if (xs >= x1) break;
+              // the next sequence with tokens
+              unsigned some = 0u;
+              for (++b; b < p.B && some == 0u; b += 32) {
+                some = __ballot_sync(0xffffffffu, b + lane < p.B && pf_seq(a, b + lane, false).n > 0);
+                if (some != 0u) b += __ffs(some) - 1 - 32;
+              }
+              if (some == 0u) break;
+              s = pf_seq(a, b, false);
+            }
+          }
+        }
+      }
+      if (lane == 0) {
+        a.joins[2 * cta] = join0;
+        a.joins[2 * cta + 1] = join1;
+      }
+      // the end of the pieces
+      if (ok && __all_sync(0xffffffffu, ui < kPfRing || mbar_wait(unit_empty(ui % kPfRing), ((ui / kPfRing) - 1) & 1,
+                                                                   abort_flag))) {
+        if (lane == 0) {
+          ring[16 * (ui % kPfRing) + kHead] = -1;
+          mbar_arrive(unit_full(ui % kPfRing));
+        }
+      }
+      // Copies still in flight must land before the CTA may exit.
+      if (lane == 0) {
+        if (ui > 0) {
+          mbar_wait_drain(q_full(0), (ui - 1) & 1);
+          mbar_wait_drain(q_full(1), (ui - 1) & 1);
+        }
+        for (int i = max(0, it - NS); i < it; ++i) {
+          const int slot = i % NS;
+          if ((slot_tail >> slot) & 1u) mbar_wait_drain(tail(slot), ((tail_uses >> slot) & 1u) ^ 1u);
+          else mbar_wait_drain(kv_full(slot), (i / NS) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kPfTailWarp) {
+      // ------------------------------------------------ cleaner of V's last tile
+      int it_base = 0;
+      uint32_t tail_uses = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int r = 0; ok; ++r) {
+        volatile int* const e = next_piece(r, ok);
+        if (e == nullptr) break;
+        const int L = e[kKeys], steps = e[kSteps], j_last = e[kJ0] + steps - 1;
+        release(r);
+        if (steps > 0 && (j_last + 1) * 128 > L) {
+          const int itv = it_base + 2 * steps - 1;
+          const int slot = itv % NS;
+          if (!__all_sync(0xffffffffu, mbar_wait(tail(slot), (tail_uses >> slot) & 1u, abort_flag))) break;
+          tail_uses ^= 1u << slot;
+          // rows L mod 128 .. 127 (those behind the last page are zeros already)
+          const int first = L - j_last * 128;
+          const int stop = min(128, (((L - 1) >> p.page_shift) + 1 << p.page_shift) - j_last * 128);
+          for (int blk = 0; blk < Cfg::kBlocks; ++blk)
+            for (int c = first * 8 + lane; c < stop * 8; c += 32)
+              st_shared_zero16(sKV + slot * Cfg::kTileBytes + blk * Cfg::kBlockBytes + c * 16);
+          fence_async_shared();  // the MMAs read shared memory through the async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_full(slot));
+        }
+        it_base += 2 * steps;
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------- MMA issuer of tile t
+      // As in prefill.cuh; in a thin piece tile t takes key tiles t, t + 2, ...
+      // and releases their slots for both issuers.
+      const int t = (warp == kMmaWarp) ? 0 : 1;
+      if (lane == 0) {
+        const uint64_t hi = static_cast<uint64_t>(sdesc_hi(1024)) << 32;
+        const uint64_t dq = hi | sdesc_lo(sQ + t * Cfg::kTileBytes, 16);
+        auto dk = [&](int slot) { return hi | sdesc_lo(sKV + slot * Cfg::kTileBytes, 16); };
+        auto dv = [&](int slot) { return hi | sdesc_lo(sKV + slot * Cfg::kTileBytes, Cfg::kBlockBytes); };
+        const uint32_t tS = tmem + t * 128;
+        const uint32_t tO = tmem + 2 * 128 + t * D;
+        int it_base = 0, seg = 0, pj = 0, ui = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int r = 0; ok; ++r) {
+          volatile int* const e = next_piece(r, ok);
+          if (e == nullptr) break;
+          const int n0 = e[kN0], n1 = e[kN1], steps = e[kSteps];
+          const bool thin = e[kThin] != 0;
+          release(r);
+          const int nt = t ? n1 : n0;
+          const int n_max = max(n0, n1);
+          const int n_slots = thin ? nt : n_max;  // key tiles whose slots this thread releases
+          if (!mbar_wait(q_full(t), ui & 1, abort_flag)) break;
+          if (nt == 0) mma_commit(q_empty(t));
+#pragma unroll 1
+          for (int k = 0; k <= n_max; ++k, ++seg) {
+            int slot_v = -1, slot_k = -1;
+            if (k >= 1 && k <= n_slots) {
+              const int x = thin ? 2 * (k - 1) + t : k - 1;
+              const int itv = it_base + 2 * x + 1;
+              slot_v = itv % NS;
+              if (!mbar_wait(kv_full(slot_v), (itv / NS) & 1, abort_flag) ||
+                  (k - 1 < nt && !mbar_wait(p_full(t), pj & 1, abort_flag))) {
+                ok = false;
+                break;
+              }
+            }
+            if (k < n_slots) {
+              const int x = thin ? 2 * k + t : k;
+              const int itk = it_base + 2 * x;
+              slot_k = itk % NS;
+              if (!mbar_wait(kv_full(slot_k), (itk / NS) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+            }
+            if (t == 1) {
+              if (!mbar_wait(turn(1), seg & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+            } else if (seg >= 1) {
+              if (!mbar_wait(turn(0), (seg - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+            }
+            tc_fence_after();
+            if (k >= 1 && k - 1 < nt) {
+              const uint64_t v_desc = dv(slot_v);
+              issue_pv<D, 0>(tO, tS, v_desc, k > 1);
+              issue_pv<D, 1>(tO, tS, v_desc, true);
+              ++pj;
+              if (k == nt) mma_commit(o_full(t));
+            }
+            if (k < nt) {
+              issue_qk<D>(tS, dq, dk(slot_k));
+              mma_commit(s_full(t));
+              if (k == nt - 1) mma_commit(q_empty(t));
+            }
+            if (slot_v >= 0) {
+              mma_commit(kv_empty(slot_v));
+              if (thin) mma_commit(kv_empty(slot_v));
+            }
+            if (slot_k >= 0) {
+              mma_commit(kv_empty(slot_k));
+              if (thin) mma_commit(kv_empty(slot_k));
+            }
+            mbar_arrive(turn(1 - t));
+          }
+          it_base += 2 * steps;
+          ++ui;
+        }
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // Warpgroups 0 and 1: softmax and epilogue of tile 0 and 1.
+    regs_increase<kSoftmaxRegs>();
+    const int t = warp >> 2;
+    const int wq = warp & 3;
+    const int r_in_tile = wq * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_bits + t * 128;
+    const uint32_t tO = tmem + lane_bits + 2 * 128 + t * D;
+    const float c = p.scale_log2;
+    const int tok_in_tile = static_cast<int>(fastdiv(static_cast<uint32_t>(r_in_tile), a.div_hc));
+    const int head_in_tile = r_in_tile - tok_in_tile * a.hc;
+    int sj = 0;     // S_t tiles consumed
+    int ou = 0;     // pieces whose O_t was waited for
+    int merges = 0; // thin pieces
+    bool ok = true;
+#pragma unroll 1
+    for (int r = 0; ok; ++r) {
+      volatile int* const e = next_piece(r, ok);
+      if (e == nullptr) break;
+      const int n = t ? e[kN1] : e[kN0];
+      const int n_other = t ? e[kN0] : e[kN1];
+      const bool thin = e[kThin] != 0;
+      const int L = e[kKeys];
+      const int cnt = (thin || t == 0) ? e[kCnt0] : e[kCnt1];
+      const int first_lim = e[kLim] + (thin ? 0 : t * a.tpt);  // last key that the tile's first token sees
+      const int j0 = e[kJ0] + (thin ? t : 0), j_step = thin ? 2 : 1;
+      const bool live = tok_in_tile < cnt && head_in_tile < e[kHeads];
+      const int row_lim = p.causal ? min(L - 1, first_lim + tok_in_tile) : L - 1;
+      // a warp without rows takes part in the hand-offs only
+      const bool idle = static_cast<int>(fastdiv(static_cast<uint32_t>(wq * 32), a.div_hc)) >= cnt;
+      const int row_tok = live ? e[kTok0] + (thin ? 0 : t * a.tpt) + tok_in_tile : -1;
+      const int row_head = e[kG0] + head_in_tile;
+      const int slot = e[kSlot];
+      release(r);
+      float m_used = -INFINITY;
+      float l = 0.f;
+
+#pragma unroll 1
+      for (int k = 0; k < n; ++k, ++sj) {
+        if (!mbar_wait(s_full(t), sj & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          uint32_t sv[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[q * 32]));
+          tmem_wait_ld();
+          const int k0 = (j0 + k * j_step) * 128;
+          if (k0 + 128 > L || (p.causal && k0 + 127 > first_lim)) {
+            const int lim = row_lim - k0;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > lim) sv[i] = __float_as_uint(-INFINITY);
+          }
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) {
+            mx0 = max3f(mx0, __uint_as_float(sv[i + 0]), __uint_as_float(sv[i + 1]));
+            mx1 = max3f(mx1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+            mx2 = max3f(mx2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
+            mx3 = max3f(mx3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+          }
+          const float m_new = max3f(m_used, max3f(mx0, mx1, mx2), mx3);
+          const bool rescale = (m_new - m_used) * c > kRescaleThreshold;
+          float alpha = 1.f;
+          if (rescale) {
+            alpha = ex2_approx((m_used - m_new) * c);
+            m_used = m_new;
+            l *= alpha;
+          }
+          if (k > 0 && __any_sync(0xffffffffu, rescale)) {
+            const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + q * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 rr = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2);
+                o[i] = __float_as_uint(rr.x);
+                o[i + 1] = __float_as_uint(rr.y);
+              }
+              tmem_st32(tO + q * 32, o);
+            }
+          }
+          const float mc = (m_used == -INFINITY) ? 0.f : m_used * c;
+          const float2 c2 = make_float2(c, c);
+          const float2 nmc2 = make_float2(-mc, -mc);
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e2 = 0; e2 < 64; e2 += 4) {
+              const int i = half * 64 + e2;
+              const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2, nmc2);
+              const float2 y1 =
+                  __ffma2_rn(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), c2, nmc2);
+              const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+              const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+              acc0 = __fadd2_rn(acc0, p0);
+              acc1 = __fadd2_rn(acc1, p1);
+              // the product with V takes bf16: one rounding of every probability
+              pk[e2 / 2] = pack_bf16x2(p0.x, p0.y);
+              pk[e2 / 2 + 1] = pack_bf16x2(p1.x, p1.y);
+            }
+            tmem_st32(tS + half * 32, pk);
+          }
+          tmem_wait_st();
+          l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
+      }
+      if (!ok) break;
+
+      // ---- epilogue
+      if (n > 0) {
+        if (!mbar_wait(o_full(t), ou & 1, abort_flag)) ok = false;
+        ++ou;
+      }
+      tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;  // thin: weights of the two tiles' outputs
+      bool have_other = false;
+      if (thin) {
+        if (t == 1) {
+          // leave (max, sum) to tile 0's warps and wait until they have read O_1
+          merge_ml[r_in_tile] = make_float2(m_used, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(merge_full);
+          if (!mbar_wait(merge_done, merges & 1, abort_flag)) ok = false;
+          ++merges;
+          tc_fence_after();
+          continue;
+        }
+        if (!mbar_wait(merge_full, merges & 1, abort_flag)) ok = false;
+        ++merges;
+        tc_fence_after();
+        const float2 o = merge_ml[r_in_tile];
+        const float l1 = n_other > 0 && !idle ? o.y : 0.f;
+        have_other = n_other > 0;
+        const float M = fmaxf(l > 0.f ? m_used : -INFINITY, l1 > 0.f ? o.x : -INFINITY);
+        w0 = l > 0.f ? ex2_approx((m_used - M) * c) : 0.f;
+        w1 = l1 > 0.f ? ex2_approx((o.x - M) * c) : 0.f;
+        m_used = M;
+        l = l * w0 + l1 * w1;
+      }
+      const bool empty_row = (m_used == -INFINITY) || !(l > 0.f);
+      const float inv_l = empty_row ? 0.f : 1.f / l;
+      const bool have_o = __all_sync(0xffffffffu, ok && n > 0);  // collective loads: warp-uniform
+      have_other = __all_sync(0xffffffffu, ok && have_other);
+      const float2 s0 = make_float2(w0 * inv_l, w0 * inv_l), s1 = make_float2(w1 * inv_l, w1 * inv_l);
+      // 32 columns of this row, normalised
+      auto load_cols = [&](int col, float2 (&f)[16]) {
+        if (have_o) {
+          uint32_t o[32];
+          tmem_ld32(tO + col, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            f[i] = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), s0);
+          if (have_other) {
+            tmem_ld32(tO + D + col, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              f[i] = __ffma2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), s1, f[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = make_float2(0.f, 0.f);
+        }
+      };
+      if (!idle && slot < 0) {
+        const int g4 = lane & 3;
+        uint16_t* dst[4];  // rows of this lane's group of four
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = __shfl_sync(0xffffffffu, row_tok, (lane & ~3) + i);
+          const int head = __shfl_sync(0xffffffffu, row_head, (lane & ~3) + i);
+          dst[i] = tok < 0 ? nullptr : p.o + (static_cast<int64_t>(tok) * p.Hq + head) * D + g4 * 16;
+        }
+        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0u;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t w[4][8];  // chunk q = columns 64 h + 16 q .. + 15 of this lane's row
+#pragma unroll
+          for (int q2 = 0; q2 < 2; ++q2) {
+            float2 f[16];
+            load_cols(h * 64 + q2 * 32, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[q2 * 2 + i / 8][i % 8] = pack_bf16x2(f[i].x, f[i].y);
+          }
+          // 4 x 4 transpose of chunks between the lanes of a group: every store
+          // of the warp then writes whole 128-byte row segments
+#pragma unroll
+          for (int sft = 2; sft > 0; sft >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i & sft) continue;
+              const int jj = i | sft;
+              const bool upper = (g4 & sft) != 0;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const uint32_t x = upper ? w[i][q] : w[jj][q];
+                const uint32_t y = __shfl_xor_sync(0xffffffffu, x, sft);
+                if (upper) {
+                  w[i][q] = y;
+                } else {
+                  w[jj][q] = y;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (dst[i] == nullptr) continue;
+            if (wide) {
+              st_global_v8(dst[i] + h * 64, w[i]);
+            } else {
+              reinterpret_cast<uint4*>(dst[i] + h * 64)[0] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+              reinterpret_cast<uint4*>(dst[i] + h * 64)[1] = make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]);
+            }
+          }
+        }
+        if (live && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(row_head) * p.T + row_tok] =
+              empty_row ? -INFINITY : (m_used * p.scale + lg2_approx(l) * 0.69314718055994531f);
+      } else if (!idle) {
+        // a partial: columns outermost, so that a warp writes 32 rows side by side
+        float* const dst = a.part_o + (static_cast<int64_t>(slot) * 2 + t) * (D * 128) + r_in_tile;
+#pragma unroll 1
+        for (int col = 0; col < D; col += 32) {
+          float2 f[16];
+          load_cols(col, f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            dst[(col + 2 * i) * 128] = f[i].x;
+            dst[(col + 2 * i + 1) * 128] = f[i].y;
+          }
+        }
+        a.part_ml[(static_cast<int64_t>(slot) * 2 + t) * 128 + r_in_tile] =
+            make_float2(empty_row ? -INFINITY : m_used * p.scale, empty_row ? 0.f : l);
+      }
+      // O_t (and in a thin piece O_1) is read: its next MMA waits for this group's next P
+      tc_fence_before();
+      if (thin) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merge_done);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Join the partials of the units that cross shares: blocks (c, tile, 32 columns) take the unit that
+// begins in CTA c's share, one thread per row, pieces in share order.
+template <int D>
+__global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const PagedParams& p = a.p;
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  const int cta = static_cast<int>(blockIdx.x), t = static_cast<int>(blockIdx.y), col = static_cast<int>(blockIdx.z) * 32;
+  const int4 j0 = a.joins[2 * cta], j1 = a.joins[2 * cta + 1];
+  if (j0.w < 0) return;
+  const int r = threadIdx.x;
+  const int tok = static_cast<int>(fastdiv(static_cast<uint32_t>(r), a.div_hc));
+  const int head = r - tok * a.hc;
+  if (tok >= (t ? j1.y : j1.x) || head >= j0.z) return;
+  const int pieces = j0.w - cta + 1;
+  auto slot = [&](int s) { return (static_cast<int64_t>(2 * (cta + s) + (s == 0 ? 1 : 0)) * 2 + t) * 128; };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < pieces; ++s) {
+    const float2 v = a.part_ml[slot(s) + r];
+    if (v.y > 0.f) M = fmaxf(M, v.x);
+  }
+  float acc[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+  float W = 0.f;
+  if (M != -INFINITY) {
+#pragma unroll 1
+    for (int s = 0; s < pieces; ++s) {
+      const float2 v = a.part_ml[slot(s) + r];
+      const float w = v.y > 0.f ? v.y * ex2_approx((v.x - M) * kLog2e) : 0.f;
+      W += w;
+      const float* src = a.part_o + slot(s) * D + static_cast<int64_t>(col) * 128 + r;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, src[i * 128], acc[i]);
+    }
+  }
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const int64_t token = j0.x + t * a.tpt + tok;
+  uint16_t* const dst = p.o + (token * p.Hq + j0.y + head) * D + col;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    *reinterpret_cast<uint4*>(dst + i) =
+        make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                   pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
+  if (col == 0 && p.lse != nullptr)
+    p.lse[static_cast<int64_t>(j0.y + head) * p.T + token] =
+        W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace sdpa

@@ -83,16 +83,16 @@ attn_status_t paged_params(PagedParams* p, const void* q, const attn_paged_cache
 }
 
 // 5-D map (64 columns, page row, 64-column block, head, page) over a pool of pages; box {64, rows,
-// d/64, 1, 1}: one copy brings `rows` rows of a page as d/64 blocks of 128-byte swizzled rows.
+// blocks, 1, 1}: one copy brings `rows` rows of a page as `blocks` blocks of 128-byte swizzled rows.
 // Without pages the map has one (of `base`, never read: its index is not a valid one).
-bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int d, int rows) {
+bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int d, int rows, int blocks) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[5] = {64, cuuint64_t{1} << p.page_shift, static_cast<cuuint64_t>(d / 64),
                               static_cast<cuuint64_t>(p.Hkv), static_cast<cuuint64_t>(std::max(p.num_pages, 1))};
   const cuuint64_t strides[4] = {static_cast<cuuint64_t>(p.sr) * 2, 128, static_cast<cuuint64_t>(p.sh) * 2,
                                  static_cast<cuuint64_t>(p.sp) * 2};
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(d / 64), 1, 1};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(blocks), 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -129,12 +129,57 @@ attn_status_t launch_paged_decode(const PagedDecodeParams& a, int sms, int dev, 
   return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-attn_status_t launch_paged_rows(const PagedParams& p, int d, cudaStream_t st) {
-  const int64_t blocks = (static_cast<int64_t>(p.T) * p.Hq + 7) / 8;
-  if (blocks > INT_MAX) return ATTN_ERR_SHAPE;
-  if (d == 128) paged_rows_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
-  else paged_rows_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+// The forward's workspace: two partial row sets of two tiles and one join per CTA of the grid.
+size_t paged_fwd_ws_bytes(int sms, int d) {
+  return static_cast<size_t>(sms) * (2 * 2 * 128 * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
+                                     2 * sizeof(int4));
+}
+
+template <int D, int NS>
+attn_status_t launch_paged_fwd(const PagedFwdParams& a, int sms, int dev, cudaStream_t st) {
+  static bool smem_done[kMaxDevices] = {};
+  static std::mutex mu;
+  using Cfg = PagedFwdCfg<D, NS>;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!smem_done[dev]) {
+      // the register split (setmaxnreg) adds up to this launch allocation, as in launch_prefill
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, paged_fwd_kernel<D, NS>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+        return ATTN_ERR_CUDA;
+    }
+    if (!set_smem(paged_fwd_kernel<D, NS>, Cfg::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kPrefillThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D, NS>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+  cfg.gridDim = dim3(static_cast<unsigned>(sms), 2, D / 32);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_fwd_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// 4-D map (d, head in group, KV head, token) over q [T, Hq, d]; box {64, hc, 1, tpt}, 128-byte swizzle.
+bool make_packed_q_map(CUtensorMap* map, const void* q, const PagedParams& p, int d, int hc, int tpt) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(p.group),
+                              static_cast<cuuint64_t>(p.Hkv), static_cast<cuuint64_t>(p.T)};
+  const cuuint64_t strides[3] = {row, row * static_cast<cuuint64_t>(p.group), row * static_cast<cuuint64_t>(p.Hq)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(hc), 1, static_cast<cuuint32_t>(tpt)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -249,23 +294,42 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
 
 size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {
   if (T < 0 || T > kMaxSeq || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return 16;
+  return paged_fwd_ws_bytes(sm_count_or_default(), d);
 }
 
 attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, const int* cu_q, const int* seqlens_k,
                              void* o, float* lse, int B, int T, int Hq, int Hkv, int d, float scale, int causal,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  PagedParams p;
-  attn_status_t s = paged_params(&p, q, cache, seqlens_k, o, lse, B, T, Hq, Hkv, d, scale, causal);
+  PagedFwdParams a;
+  std::memset(&a, 0, sizeof(a));
+  attn_status_t s = paged_params(&a.p, q, cache, seqlens_k, o, lse, B, T, Hq, Hkv, d, scale, causal);
   if (s != ATTN_OK) return s;
   if (B == 0 || T == 0) return ATTN_OK;
   if (cu_q == nullptr) return ATTN_ERR_NULL;
   if (!aligned(cu_q, 4)) return ATTN_ERR_ALIGN;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
     return ATTN_ERR_WORKSPACE;
-  if ((s = current_device(nullptr, nullptr)) != ATTN_OK) return s;
-  p.cu_q = cu_q;
-  return launch_paged_rows(p, d, static_cast<cudaStream_t>(stream));
+  int dev = 0, sms = 0;
+  if ((s = current_device(&dev, &sms)) != ATTN_OK) return s;
+  a.p.cu_q = cu_q;
+  const int group = a.p.group;
+  a.chunks = (group + 127) / 128;
+  a.hc = (group + a.chunks - 1) / a.chunks;
+  a.tpt = 128 / a.hc;
+  a.div_hc = make_fastdiv(static_cast<uint32_t>(a.hc));
+  const bool pages = a.p.num_pages > 0;
+  a.oob_page = std::max(a.p.num_pages, 1);
+  const int box = std::min(1 << a.p.page_shift, 128);
+  if (!make_packed_q_map(&a.tm_q, q, a.p, d, a.hc, a.tpt) ||
+      !make_page_map(&a.tm_k, pages ? cache->k_pages : q, a.p, d, box, 1) ||
+      !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box, 1))
+    return ATTN_ERR_CUDA;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(sms) * 4 * 128 * d);
+  a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(sms) * 4 * 128);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_paged_fwd<128, kStagesD128>(a, sms, dev, st)
+                  : launch_paged_fwd<64, kStagesD64>(a, sms, dev, st);
 }
 
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
@@ -297,8 +361,8 @@ attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t*
   const bool pages = a.p.num_pages > 0;
   a.oob_page = std::max(a.p.num_pages, 1);
   const int box = std::min(1 << a.p.page_shift, kPdKeys);
-  if (!make_page_map(&a.tm_k, pages ? cache->k_pages : q, a.p, d, box) ||
-      !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box))
+  if (!make_page_map(&a.tm_k, pages ? cache->k_pages : q, a.p, d, box, d / 64) ||
+      !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box, d / 64))
     return ATTN_ERR_CUDA;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows * d);

@@ -19,6 +19,7 @@
 #include "page_plan.cuh"
 #include "paged.cuh"
 #include "paged_decode.cuh"
+#include "paged_fwd.cuh"
 
 namespace sdpa {
 constexpr int kMaxDeviceSlots = 64;
