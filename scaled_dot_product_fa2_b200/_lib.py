@@ -108,6 +108,8 @@ def _declare(lib):
 def get():
     """The loaded library; raises if the CUDA extension has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

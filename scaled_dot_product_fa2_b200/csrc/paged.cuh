@@ -29,4 +29,10 @@ struct PagedParams {
   float scale, scale_log2;
 };
 
+// a / b of non-negative values, by the 32-bit division where both fit.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 }  // namespace sdpa

@@ -77,12 +77,6 @@ __device__ __forceinline__ int pd_tiles(int len) { return max(1, (len + kPdKeys 
 // Length of an item of sequence b on the line.
 __device__ __forceinline__ int pd_cost(const PagedParams& p, int b) { return pd_tiles(paged_len(p, b)) + kPdItemCost; }
 
-// a / b of non-negative values, by the 32-bit division where both fit.
-__device__ __forceinline__ int64_t pd_div(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 // Barrier of the consumer warps that also tells whether `pred` holds in any thread.
 __device__ __forceinline__ bool pd_any(bool pred) {
   uint32_t r;
@@ -153,8 +147,8 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
     // every share has a place at least; with fewer places than CTAs the last CTAs have none
     G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
     if (cta < G) {
-      x0 = pd_div(total * cta, G);
-      x1 = pd_div(total * (cta + 1), G);
+      x0 = div64(total * cta, G);
+      x1 = div64(total * (cta + 1), G);
     }
   };
   // Inclusive sum of t over the block's threads so far, and their total.
@@ -244,7 +238,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       int L = paged_len(p, b);
       int T = pd_tiles(L);
       const int64_t in_seq = x0 - s_prefix * per_seq;
-      int hr = static_cast<int>(pd_div(in_seq, T + kPdItemCost));
+      int hr = static_cast<int>(div64(in_seq, T + kPdItemCost));
       // places of the share that lie before the item's end: an item's first kPdItemCost places stand
       // for its fixed cost, the others for its tiles
       int64_t xs = s_prefix * per_seq + static_cast<int64_t>(hr) * (T + kPdItemCost);
@@ -280,7 +274,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
         if (tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != L) atomicOr(&g_error_word, kErrSeqlen);
         if (tile == 0 && n < T) {
           const int64_t last = xs + kPdItemCost + T;  // the CTA whose share holds the item's last tile
-          join = make_int4(b, hr, static_cast<int>(pd_div(last * G - 1, total)), 0);
+          join = make_int4(b, hr, static_cast<int>(div64(last * G - 1, total)), 0);
         }
         const int nk = L > 0 ? n : 0;
         announce(b, hr, tile, nk, L, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));

@@ -16,8 +16,8 @@
 //     second one's output is read from its own TMEM columns).
 //   * All units' keys form one line, in the order (sequence, KV head, unit), cut
 //     into equal shares, one per CTA (one CTA per SM); a share may begin and end
-//     inside a unit.  A pair's key weighs 2, a thin unit's 1, and a unit has a
-//     fixed weight besides.  A unit's visible keys are linear in its index, so
+//     inside a unit.  A key's weight depends on the unit's kind, and a
+//     unit has a fixed weight besides.  A unit's visible keys are linear in its index, so
 //     sums over a sequence's units are closed forms and every CTA finds its
 //     place from the lengths on the device.  A unit that crosses shares leaves
 //     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
@@ -34,7 +34,13 @@
 
 namespace sdpa {
 
-constexpr int kPfUnitCost = 512;   // a unit's fixed weight (two pair steps' worth of keys: measured boundary)
+// Weights on the line.  A step of 128 keys takes 2.1 us in a pair (both softmax
+// chains) and 1.6 to 1.9 us per tile in a thin unit (bound by the bytes that its
+// ring keeps in flight); a unit costs 2.4 us besides (first S, last P.V, stores).
+constexpr int kPfPair = 4, kPfThin = 3;   // per key
+constexpr int kPfUnitCost = 576;
+// Units of this many key tiles or fewer are not split: joining costs more.
+constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
 constexpr int kPfTailWarp = 11;
 
@@ -81,15 +87,15 @@ __device__ __forceinline__ int pf_visible(int causal, int64_t tokens, int L, int
 }
 
 // Weight of the first V full units (tu tokens each): V times the fixed weight
-// and twice the visible keys, which are clamp((v + 1) tu + coff, 0, L) in unit v.
+// and kPfPair times the visible keys, which are clamp((v + 1) tu + coff, 0, L) in unit v.
 __device__ __forceinline__ int64_t pf_prefix(int causal, int V, int tu, int L, int coff) {
   const int64_t fixed = static_cast<int64_t>(V) * kPfUnitCost;
-  if (!causal) return fixed + 2 * static_cast<int64_t>(V) * L;
+  if (!causal) return fixed + kPfPair * static_cast<int64_t>(V) * L;
   const int lo = min(V, max(-coff, 0) / tu);                     // units that see nothing
   const int hi = min(V, max(lo, (L - coff + tu - 1) / tu - 1));  // first unit that sees every key
   const int64_t m = hi - lo;
   const int64_t mid = m * coff + tu * (static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2;
-  return fixed + 2 * (mid + static_cast<int64_t>(V - hi) * L);
+  return fixed + kPfPair * (mid + static_cast<int64_t>(V - hi) * L);
 }
 
 __device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b, bool report) {
@@ -107,7 +113,8 @@ __device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b, bool rep
   const int rem = s.n - s.full * tu;
   s.units = s.full + (rem > 0 ? 1 : 0);
   s.cost = pf_prefix(p.causal, s.full, tu, s.L, s.coff);
-  if (rem > 0) s.cost += kPfUnitCost + (rem > a.tpt ? 2 : 1) * static_cast<int64_t>(pf_visible(p.causal, s.n, s.L, s.coff));
+  if (rem > 0)
+    s.cost += kPfUnitCost + (rem > a.tpt ? kPfPair : kPfThin) * static_cast<int64_t>(pf_visible(p.causal, s.n, s.L, s.coff));
   return s;
 }
 
@@ -206,8 +213,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   // ---- this CTA's share of the line
   const int cta = static_cast<int>(blockIdx.x);
   const int per_seq = p.Hkv * a.chunks;
-  int64_t x0 = 0, x1 = 0, total = 0;
-  int G = 0;
+  int64_t x0 = 0, x1 = 0, total = 0, quot = 0;
+  int G = 0, rem = 0;
+  auto share_begin = [&](int c) -> int64_t { return quot * c + rem * c / G; };  // floor(total * c / G)
   {
     constexpr int kWarps = kPrefillThreads / 32;
     auto cost_of = [&](int b) -> int64_t { return b < p.B ? pf_seq(a, b, cta == 0).cost : 0; };
@@ -229,12 +237,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       }
     };
     auto share = [&]() {
-      // a share is at least a pair step long (256), so each CTA between the first and the last one of
-      // a unit has a key tile of it
-      G = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), total / 256)));
+      // a share is at least a pair step long, so each CTA between the first and the last one of a
+      // unit has a key tile of it
+      G = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), total / (128 * kPfPair))));
+      quot = div64(total, G);
+      rem = static_cast<int>(total - quot * G);
       if (cta < G) {
-        x0 = total / G * cta + total % G * cta / G;
-        x1 = total / G * (cta + 1) + total % G * (cta + 1) / G;
+        x0 = share_begin(cta);
+        x1 = share_begin(cta + 1);
       }
     };
     auto find = [&](int b, int64_t t, int64_t end) {  // sequence b's weights end at `end`
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         int b = static_cast<int>(s_first);
         PfSeq s = pf_seq(a, b, false);
         const int64_t in_seq = x0 - s_prefix * per_seq;
-        int hr = static_cast<int>(in_seq / s.cost);   // KV head * chunks + head tile
+        int hr = static_cast<int>(div64(in_seq, s.cost));   // KV head * chunks + head tile
         const int64_t in_head = in_seq - hr * s.cost;
         int v = 0;
         for (int hi = s.units; hi - v > 1;) {  // last unit that begins at or before the share
@@ -315,18 +325,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           const int cnt0 = min(s.n - v * tu, a.tpt);
           const int cnt1 = min(max(s.n - v * tu - a.tpt, 0), a.tpt);
           const bool thin = cnt1 == 0;
-          const int w = thin ? 1 : 2;
+          const int w = 128 * (thin ? kPfThin : kPfPair);  // weight of a key tile
           const int64_t t0 = static_cast<int64_t>(v) * tu;
           const int keys = pf_visible(p.causal, t0 + cnt0 + cnt1, s.L, s.coff);
           const int n_u = (keys + 127) / 128;                                          // its key tiles
           const int n_0 = (pf_visible(p.causal, t0 + cnt0, s.L, s.coff) + 127) / 128;  // tile 0's
-          // key tile k stands at xs + kPfUnitCost + 128 w k
+          // key tile k stands at xs + kPfUnitCost + w k
+          const bool split = n_u > (thin ? kPfWholeThin : kPfWholePair);
           auto tile_at = [&](int64_t x) -> int {
             const int64_t off = x - xs - kPfUnitCost;
-            return off <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(n_u), (off + 128 * w - 1) / (128 * w)));
+            if (off <= 0) return 0;
+            return split ? static_cast<int>(min(static_cast<int64_t>(n_u), div64(off + w - 1, w))) : n_u;
           };
           const int j0 = tile_at(x0), j1 = tile_at(x1);
-          const int64_t xe = xs + kPfUnitCost + static_cast<int64_t>(w) * keys;
+          const int64_t xe = xs + kPfUnitCost + static_cast<int64_t>(w / 128) * keys;
           if (j1 > j0 || (n_u == 0 && xs >= x0)) {
             const int steps = j1 - j0;
             const bool whole = steps == n_u;
@@ -343,10 +355,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               n1 = steps;
             }
             if (j0 == 0 && !whole) {
-              const int64_t last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * 128 * w;
+              const int64_t last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * w;
               // the CTA whose share holds the unit's last key tile
-              int c = static_cast<int>(last / (total / G + 1));  // at most the right one
-              while (c + 1 < G && total / G * (c + 1) + total % G * (c + 1) / G <= last) ++c;
+              int c = static_cast<int>(div64(last, quot + 1));  // at most the right one
+              while (c + 1 < G && share_begin(c + 1) <= last) ++c;
               join0 = make_int4(tok0, hk * p.group + g0, heads, c);
               join1 = make_int4(cnt0, cnt1, 0, 0);
             }
@@ -392,12 +404,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               }
               return true;
             };
-            if (steps <= 1) ok = load_q();
             int page = page_of(b, j0, s.L);
+            const bool q_first = steps <= 1 || ui == 0;  // nothing to wait for
+            if (q_first) ok = load_q();
 #pragma unroll 1
             for (int x = 0; ok && x < steps; ++x) {
               const int j = j0 + x;
-              if (x == 1 && !load_q()) {  // after K_0, V_0
+              if (x == 1 && !q_first && !load_q()) {  // after K_0, V_0
                 ok = false;
                 break;
               }
@@ -854,15 +867,18 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   }
 }
 
-// Join the partials of the units that cross shares: blocks (c, tile, 32 columns) take the unit that
+// Join the partials of the units that cross shares: blocks (c, tile, 16 columns) take the unit that
 // begins in CTA c's share, one thread per row, pieces in share order.
+constexpr int kPfJoinCols = 16;
+
 template <int D>
 __global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a) {
   constexpr float kLog2e = 1.4426950408889634f;
   const PagedParams& p = a.p;
   grid_dependency_trigger();
   grid_dependency_wait();
-  const int cta = static_cast<int>(blockIdx.x), t = static_cast<int>(blockIdx.y), col = static_cast<int>(blockIdx.z) * 32;
+  const int cta = static_cast<int>(blockIdx.x), t = static_cast<int>(blockIdx.y);
+  const int col = static_cast<int>(blockIdx.z) * kPfJoinCols;
   const int4 j0 = a.joins[2 * cta], j1 = a.joins[2 * cta + 1];
   if (j0.w < 0) return;
   const int r = threadIdx.x;
@@ -871,32 +887,42 @@ __global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_consta
   if (tok >= (t ? j1.y : j1.x) || head >= j0.z) return;
   const int pieces = j0.w - cta + 1;
   auto slot = [&](int s) { return (static_cast<int64_t>(2 * (cta + s) + (s == 0 ? 1 : 0)) * 2 + t) * 128; };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < pieces; ++s) {
-    const float2 v = a.part_ml[slot(s) + r];
-    if (v.y > 0.f) M = fmaxf(M, v.x);
-  }
-  float acc[32];
+  // one pass with a running maximum, two pieces' loads at a time
+  float M = -INFINITY, W = 0.f;
+  float acc[kPfJoinCols];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-  float W = 0.f;
-  if (M != -INFINITY) {
+  for (int i = 0; i < kPfJoinCols; ++i) acc[i] = 0.f;
 #pragma unroll 1
-    for (int s = 0; s < pieces; ++s) {
-      const float2 v = a.part_ml[slot(s) + r];
-      const float w = v.y > 0.f ? v.y * ex2_approx((v.x - M) * kLog2e) : 0.f;
-      W += w;
-      const float* src = a.part_o + slot(s) * D + static_cast<int64_t>(col) * 128 + r;
+  for (int s0 = 0; s0 < pieces; s0 += 2) {
+    float2 ml[2];
+    float x[2][kPfJoinCols];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, src[i * 128], acc[i]);
+    for (int u = 0; u < 2; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (s0 + u < pieces) {
+        ml[u] = a.part_ml[slot(s0 + u) + r];
+        const float* src = a.part_o + slot(s0 + u) * D + static_cast<int64_t>(col) * 128 + r;
+#pragma unroll
+        for (int i = 0; i < kPfJoinCols; ++i) x[u][i] = src[i * 128];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!(ml[u].y > 0.f)) continue;
+      const float m_new = fmaxf(M, ml[u].x);
+      const float down = M == -INFINITY ? 0.f : ex2_approx((M - m_new) * kLog2e);
+      const float w = ml[u].y * ex2_approx((ml[u].x - m_new) * kLog2e);
+      M = m_new;
+      W = W * down + w;
+#pragma unroll
+      for (int i = 0; i < kPfJoinCols; ++i) acc[i] = fmaf(w, x[u][i], acc[i] * down);
     }
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
   const int64_t token = j0.x + t * a.tpt + tok;
   uint16_t* const dst = p.o + (token * p.Hq + j0.y + head) * D + col;
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < kPfJoinCols; i += 8)
     *reinterpret_cast<uint4*>(dst + i) =
         make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
                    pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));

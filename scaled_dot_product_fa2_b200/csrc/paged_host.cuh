@@ -161,7 +161,7 @@ attn_status_t launch_paged_fwd(const PagedFwdParams& a, int sms, int dev, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D, NS>, a) != cudaSuccess) return ATTN_ERR_CUDA;
-  cfg.gridDim = dim3(static_cast<unsigned>(sms), 2, D / 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(sms), 2, D / kPfJoinCols);
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_fwd_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

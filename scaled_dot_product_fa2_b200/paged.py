@@ -1,5 +1,10 @@
 """Torch-facing wrappers of the paged KV cache's entry points (argument
-marshalling only, as in ``ops``)."""
+marshalling only, as in ``ops``).
+
+A decode step's kernels take a few microseconds, so what a wrapper does before
+the launch counts: each property of a tensor is read once, a device is compared
+by its index, and the device context is entered only where it changes something.
+"""
 from __future__ import annotations
 
 import ctypes
@@ -7,83 +12,105 @@ import ctypes
 import torch
 
 from . import _lib
-from .ops import CAUSAL_BOTTOM_RIGHT, LAYOUT_BHSD, LAYOUT_BSHD, _check_lengths, _check_tensor, _stream_handle
+from .ops import CAUSAL_BOTTOM_RIGHT, LAYOUT_BHSD, LAYOUT_BSHD, _stream_handle
+
+_BF16, _INT32, _FP32 = torch.bfloat16, torch.int32, torch.float32
+# the current stream of a device as an integer, without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream_handle
 
 
-def _check_ints(name, t, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
-        raise TypeError(f"{name} must be an int32 tensor")
-    if tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}, got {tuple(t.shape)}")
+def _call(fn, name, index, *args):
+    """One entry point on the current stream of device `index`."""
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _lib.check(st, name)
 
 
-def _check_pages(name, t):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
-    if not t.is_cuda:
+def _tensor(name, t, dtype, ndim):
+    """The device index of a contiguous CUDA tensor of this type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    index = t.get_device() if t.is_cuda else -1
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    _, s1, s2, d = t.shape
-    if t.stride()[1:] != (s2 * d, d, 1):
-        raise ValueError(f"{name} must be dense inside a page")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return index
 
 
-def _paged_cache(k_pages, v_pages, layout, device, block_table=None):
+def _ints(name, t, n, index):
+    """The address of a contiguous int32 tensor [n] on device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.dim() != 1:
+        raise TypeError(f"{name} must be an int32 tensor [{n}]")
+    if t.numel() != n or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor on cuda:{index}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _table(t, B, index):
+    """(address, entries per row) of a block table."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.dim() != 2:
+        raise TypeError("block_table must be an int32 tensor [B, max_pages]")
+    rows, width = t.shape
+    if rows != B or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous [{B}, max_pages] tensor on cuda:{index}")
+    return t.data_ptr(), width
+
+
+def _pages(k_pages, v_pages, layout, index, table=0, max_pages=0):
     """(attn_paged_cache_t, Hkv, d) of two page pools [N, Hkv, P, d] ([N, P, Hkv, d] for
     LAYOUT_BSHD), dense inside a page and of one stride between pages."""
-    _check_pages("k_pages", k_pages)
-    _check_pages("v_pages", v_pages)
-    if layout == LAYOUT_BSHD:
-        N, P, Hkv, d = k_pages.shape
-    elif layout == LAYOUT_BHSD:
-        N, Hkv, P, d = k_pages.shape
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+            raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
+        if not t.is_cuda or t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}")
+    shape = k_pages.shape
+    N, s1, s2, d = shape
+    sk, sv = k_pages.stride(), v_pages.stride()
+    dense = (s2 * d, d, 1)
+    if sk[1:] != dense or sv[1:] != dense:
+        raise ValueError("k_pages and v_pages must be dense inside a page")
+    if v_pages.shape != shape or (N > 1 and sk[0] != sv[0]):
+        raise ValueError("k_pages and v_pages must have one shape and one page stride")
+    if layout == LAYOUT_BHSD:
+        Hkv, P = s1, s2
+    elif layout == LAYOUT_BSHD:
+        P, Hkv = s1, s2
     else:
         raise ValueError(f"unknown layout {layout}")
-    if v_pages.shape != k_pages.shape or (N > 1 and v_pages.stride(0) != k_pages.stride(0)):
-        raise ValueError("k_pages and v_pages must have one shape and one page stride")
-    if k_pages.device != device or v_pages.device != device:
-        raise ValueError(f"k_pages and v_pages must be on {device}")
-    c = _lib.PagedCache()
-    c.k_pages = k_pages.data_ptr()
-    c.v_pages = v_pages.data_ptr()
-    c.page_stride = k_pages.stride(0) if N > 1 else 0
-    c.num_pages = N
-    c.page_size = P
-    c.layout = int(layout)
-    if block_table is not None:
-        c.block_table = block_table.data_ptr()
-        c.max_pages = int(block_table.shape[1])
-    return c, Hkv, d
+    return _lib.PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), table, sk[0] if N > 1 else 0, N, P, max_pages,
+                           layout), Hkv, d
 
 
-def _check_table(block_table, B, device):
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2:
-        raise TypeError("block_table must be an int32 tensor [B, max_pages]")
-    if block_table.shape[0] != B or block_table.device != device or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous [{B}, max_pages] tensor on {device}")
-
-
-def _outputs(q, lse_shape, out, lse, return_lse):
+def _outputs(q, lse_shape, out, lse, return_lse, index):
     if out is None:
         out = torch.zeros_like(q)
-    else:
-        _check_tensor("out", out, torch.bfloat16, q.dim())
-        if out.shape != q.shape or out.device != q.device:
-            raise ValueError("out must have the shape of q, on q's device")
+    elif _tensor("out", out, _BF16, q.dim()) != index or out.shape != q.shape:
+        raise ValueError("out must have the shape of q, on q's device")
     if lse is None:
         if return_lse:
-            lse = torch.zeros(lse_shape, dtype=torch.float32, device=q.device)
-    else:
-        _check_tensor("lse", lse, torch.float32, len(lse_shape))
-        if tuple(lse.shape) != lse_shape or lse.device != q.device:
-            raise ValueError(f"lse must be {list(lse_shape)} on q's device")
+            lse = torch.zeros(lse_shape, dtype=_FP32, device=q.device)
+    elif _tensor("lse", lse, _FP32, len(lse_shape)) != index or lse.shape != lse_shape:
+        raise ValueError(f"lse must be {list(lse_shape)} on q's device")
     return out, lse
 
 
-def _check_workspace(workspace, device):
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+def _workspace(t, index):
+    """(address, bytes) of a workspace."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous buffer on q's device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def attn_page_plan(past_lens, new_lens, block_table, free_pages, free_range, page_size: int, num_tokens: int,
@@ -99,38 +126,29 @@ def attn_page_plan(past_lens, new_lens, block_table, free_pages, free_range, pag
     or ``new_lens`` and ``free_range_out`` may be ``free_range``.  Refused requests are
     reported by check_device_error (ATTN_ERR_PAGE).
     """
-    if not isinstance(past_lens, torch.Tensor) or past_lens.dim() != 1:
-        raise TypeError("past_lens must be an int32 tensor [B]")
-    if not past_lens.is_cuda:
-        raise ValueError("past_lens must be a CUDA tensor")
-    B, dev = past_lens.shape[0], past_lens.device
-    _check_lengths("past_lens", past_lens, B, dev)
-    _check_lengths("new_lens", new_lens, B, dev)
-    _check_table(block_table, B, dev)
+    index = _tensor("past_lens", past_lens, _INT32, 1)
+    B = past_lens.shape[0]
+    new = _ints("new_lens", new_lens, B, index)
+    table, width = _table(block_table, B, index)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise TypeError("free_pages must be an int32 tensor [num_free]")
-    _check_ints("free_pages", free_pages, (free_pages.shape[0],), dev)
-    _check_ints("free_range", free_range, (2,), dev)
+    num_free = free_pages.shape[0]
+    free = _ints("free_pages", free_pages, num_free, index)
+    frange = _ints("free_range", free_range, 2, index)
     T = int(num_tokens)
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    outs = []
-    for name, t, n in (("cu_new", cu_new, B + 1), ("total_lens", total_lens, B), ("positions", positions, T),
-                       ("slot_map", slot_map, T), ("free_range_out", free_range_out, 2)):
-        if t is None:
-            t = torch.empty(n, dtype=torch.int32, device=dev)
-        else:
-            _check_ints(name, t, (n,), dev)
-        outs.append(t)
-    lib = _lib.get()
-    with torch.cuda.device(dev):
-        st = lib.attn_page_plan(past_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                                free_pages.data_ptr(), free_range.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
-                                outs[2].data_ptr(), outs[3].data_ptr(), outs[4].data_ptr(), B,
-                                int(block_table.shape[1]), int(free_pages.shape[0]), int(page_size), T,
-                                _stream_handle(dev))
-    _lib.check(st, "attn_page_plan")
-    return tuple(outs)
+    if cu_new is None or total_lens is None or positions is None or slot_map is None or free_range_out is None:
+        def new_ints(t, n):
+            return torch.empty(n, dtype=_INT32, device=past_lens.device) if t is None else t
+        cu_new, total_lens = new_ints(cu_new, B + 1), new_ints(total_lens, B)
+        positions, slot_map = new_ints(positions, T), new_ints(slot_map, T)
+        free_range_out = new_ints(free_range_out, 2)
+    _call(_lib.get().attn_page_plan, "attn_page_plan", index, past_lens.data_ptr(), new, table, free, frange,
+          _ints("cu_new", cu_new, B + 1, index), _ints("total_lens", total_lens, B, index),
+          _ints("positions", positions, T, index), _ints("slot_map", slot_map, T, index),
+          _ints("free_range_out", free_range_out, 2, index), B, width, num_free, int(page_size), T)
+    return cu_new, total_lens, positions, slot_map, free_range_out
 
 
 def attn_rope_append_paged(packed_qkv, cos, sin, positions, slot_map, k_pages, v_pages, Hq: int, Hkv: int,
@@ -142,30 +160,21 @@ def attn_rope_append_paged(packed_qkv, cos, sin, positions, slot_map, k_pages, v
     LAYOUT_BSHD), updated in place.  Returns q [T, Hq, d]; rows of tokens with a negative slot
     are not written (a new ``q_out`` is zero-filled).
     """
-    _check_tensor("packed_qkv", packed_qkv, torch.bfloat16, 2)
-    _check_tensor("cos", cos, torch.float32, 2)
-    _check_tensor("sin", sin, torch.float32, 2)
+    index = _tensor("packed_qkv", packed_qkv, _BF16, 2)
     T, width = packed_qkv.shape
-    dev = packed_qkv.device
-    cache, pages_hkv, d = _paged_cache(k_pages, v_pages, layout, dev)
+    cache, pages_hkv, d = _pages(k_pages, v_pages, layout, index)
     if pages_hkv != Hkv or Hq <= 0 or width != (Hq + 2 * Hkv) * d:
         raise ValueError("packed_qkv's last dim must be (Hq + 2*Hkv) * d of pages with Hkv heads")
-    if cos.shape != sin.shape or cos.shape[1] != d // 2 or cos.device != dev or sin.device != dev:
+    if _tensor("cos", cos, _FP32, 2) != index or _tensor("sin", sin, _FP32, 2) != index or cos.shape != sin.shape \
+            or cos.shape[1] != d // 2:
         raise ValueError("cos and sin must both be [max_pos, d/2] on packed_qkv's device")
-    _check_ints("positions", positions, (T,), dev)
-    _check_ints("slot_map", slot_map, (T,), dev)
+    pos, slot = _ints("positions", positions, T, index), _ints("slot_map", slot_map, T, index)
     if q_out is None:
-        q_out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_tensor("q_out", q_out, torch.bfloat16, 3)
-        if tuple(q_out.shape) != (T, Hq, d) or q_out.device != dev:
-            raise ValueError(f"q_out must be {(T, Hq, d)} on packed_qkv's device")
-    lib = _lib.get()
-    with torch.cuda.device(dev):
-        st = lib.attn_rope_append_paged(packed_qkv.data_ptr(), cos.data_ptr(), sin.data_ptr(), int(cos.shape[0]),
-                                        positions.data_ptr(), slot_map.data_ptr(), q_out.data_ptr(),
-                                        ctypes.byref(cache), T, Hq, Hkv, d, _stream_handle(dev))
-    _lib.check(st, "attn_rope_append_paged")
+        q_out = torch.zeros((T, Hq, d), dtype=_BF16, device=packed_qkv.device)
+    elif _tensor("q_out", q_out, _BF16, 3) != index or q_out.shape != (T, Hq, d):
+        raise ValueError(f"q_out must be {(T, Hq, d)} on packed_qkv's device")
+    _call(_lib.get().attn_rope_append_paged, "attn_rope_append_paged", index, packed_qkv.data_ptr(), cos.data_ptr(),
+          sin.data_ptr(), cos.shape[0], pos, slot, q_out.data_ptr(), ctypes.byref(cache), T, Hq, Hkv, d)
     return q_out
 
 
@@ -209,29 +218,21 @@ def attn_fwd_paged(q, k_pages, v_pages, cu_q, seqlens_k, block_table, causal: in
     keys per sequence; block_table [B, max_pages] int32.  Returns (o [T, Hq, d], lse [Hq, T]
     fp32); rows behind cu_q[B] are not written (new buffers are zero-filled).
     """
-    _check_tensor("q", q, torch.bfloat16, 3)
+    index = _tensor("q", q, _BF16, 3)
     T, Hq, d = q.shape
-    dev = q.device
     if not isinstance(seqlens_k, torch.Tensor) or seqlens_k.dim() != 1:
         raise TypeError("seqlens_k must be an int32 tensor [B]")
     B = seqlens_k.shape[0]
-    _check_lengths("seqlens_k", seqlens_k, B, dev)
-    _check_ints("cu_q", cu_q, (B + 1,), dev)
-    _check_table(block_table, B, dev)
-    cache, Hkv, dk = _paged_cache(k_pages, v_pages, layout, dev, block_table)
+    lens, cu = _ints("seqlens_k", seqlens_k, B, index), _ints("cu_q", cu_q, B + 1, index)
+    cache, Hkv, dk = _pages(k_pages, v_pages, layout, index, *_table(block_table, B, index))
     if dk != d:
         raise ValueError(f"head_dim of q ({d}) and of the pages ({dk}) differ")
-    out, lse = _outputs(q, (Hq, T), out, lse, return_lse)
+    out, lse = _outputs(q, (Hq, T), out, lse, return_lse, index)
     if workspace is None:
         workspace = fwd_paged_workspace(q, k_pages, layout)
-    _check_workspace(workspace, dev)
-    lib = _lib.get()
-    with torch.cuda.device(dev):
-        st = lib.attn_fwd_paged(q.data_ptr(), ctypes.byref(cache), cu_q.data_ptr(), seqlens_k.data_ptr(),
-                                out.data_ptr(), lse.data_ptr() if lse is not None else None, B, T, Hq, Hkv, d,
-                                float(scale), int(causal), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_handle(dev))
-    _lib.check(st, "attn_fwd_paged")
+    ws, ws_bytes = _workspace(workspace, index)
+    _call(_lib.get().attn_fwd_paged, "attn_fwd_paged", index, q.data_ptr(), ctypes.byref(cache), cu, lens,
+          out.data_ptr(), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, d, scale, causal, ws, ws_bytes)
     return out, lse
 
 
@@ -243,23 +244,17 @@ def attn_decode_splitkv_paged(q, k_pages, v_pages, seqlens_k, block_table, causa
     q [B, Sq, Hq, d] bf16 (token-major, as attn_rope_append_paged writes it); pages, lengths and
     table as for attn_fwd_paged.  Returns (o [B, Sq, Hq, d], lse [B, Hq, Sq] fp32).
     """
-    _check_tensor("q", q, torch.bfloat16, 4)
+    index = _tensor("q", q, _BF16, 4)
     B, Sq, Hq, d = q.shape
-    dev = q.device
-    _check_lengths("seqlens_k", seqlens_k, B, dev)
-    _check_table(block_table, B, dev)
-    cache, Hkv, dk = _paged_cache(k_pages, v_pages, layout, dev, block_table)
+    lens = _ints("seqlens_k", seqlens_k, B, index)
+    cache, Hkv, dk = _pages(k_pages, v_pages, layout, index, *_table(block_table, B, index))
     if dk != d:
         raise ValueError(f"head_dim of q ({d}) and of the pages ({dk}) differ")
-    out, lse = _outputs(q, (B, Hq, Sq), out, lse, return_lse)
+    out, lse = _outputs(q, (B, Hq, Sq), out, lse, return_lse, index)
     if workspace is None:
         workspace = decode_paged_workspace(q, k_pages, layout)
-    _check_workspace(workspace, dev)
-    lib = _lib.get()
-    with torch.cuda.device(dev):
-        st = lib.attn_decode_splitkv_paged(q.data_ptr(), ctypes.byref(cache), seqlens_k.data_ptr(), out.data_ptr(),
-                                           lse.data_ptr() if lse is not None else None, B, Hq, Hkv, Sq, d,
-                                           float(scale), int(causal), workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), _stream_handle(dev))
-    _lib.check(st, "attn_decode_splitkv_paged")
+    ws, ws_bytes = _workspace(workspace, index)
+    _call(_lib.get().attn_decode_splitkv_paged, "attn_decode_splitkv_paged", index, q.data_ptr(),
+          ctypes.byref(cache), lens, out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, Sq, d,
+          scale, causal, ws, ws_bytes)
     return out, lse
