@@ -9,9 +9,14 @@
 // j <= i + L_b - n_b.  Keys that are not visible are never read, so whatever a
 // page holds behind a sequence's last key has no effect.
 #pragma once
+#include "fastdiv.h"
 #include "ptx.cuh"
 
 namespace sdpa {
+
+// A sequence of the forward's batch that brings no more query rows of a KV head
+// than this (a single token, mostly) is the decode's work.
+constexpr int kRowUnit = 16;
 
 struct PagedParams {
   const uint16_t* q;   // [T][Hq][d] bf16 (the decode: T = B * Sq)
@@ -27,7 +32,38 @@ struct PagedParams {
   int num_pages, max_pages, page_shift;
   int causal;          // 0 none, 1 top-left, 2 bottom-right
   float scale, scale_log2;
+  FastDiv div_group;
+  int row_tokens;      // tokens of a sequence that is the decode's work: kRowUnit / group
 };
+
+// A number of keys, clamped to what a row of the table can hold (2^30 at most).
+__device__ __forceinline__ int paged_clamp(const PagedParams& p, int len) {
+  return min(max(len, 0), p.max_pages << p.page_shift);
+}
+
+// Keys that the first `tokens` tokens of a sequence see together: token i sees
+// key j iff j < L and, under a causal mask, j <= i + coff.
+__device__ __forceinline__ int paged_visible(int causal, int64_t tokens, int L, int coff) {
+  return causal ? static_cast<int>(min(max(tokens + coff, int64_t{0}), static_cast<int64_t>(L))) : L;
+}
+
+// A ragged sequence's first token, its tokens and its keys, clamped to the
+// batch and the table (`bad`: something was).
+struct PagedSeq {
+  int start, n, L;
+  bool bad;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), raw = __ldg(p.lens + b);
+  PagedSeq s;
+  s.start = min(max(c0, 0), p.T);
+  const int end = min(max(c1, s.start), p.T);
+  s.n = end - s.start;
+  s.L = paged_clamp(p, raw);
+  s.bad = s.start != c0 || end != c1 || s.L != raw;
+  return s;
+}
 
 // a / b of non-negative values, by the 32-bit division where both fit.
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {

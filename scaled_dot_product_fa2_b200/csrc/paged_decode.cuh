@@ -1,4 +1,5 @@
-// paged_decode.cuh -- split-KV decode attention over a paged KV cache.
+// paged_decode.cuh -- split-KV decode attention over a paged KV cache, and the short
+// sequences of the paged forward.
 //
 // A work item is (sequence, KV head, group of up to 16 query rows that share
 // the head); its keys are walked in tiles of 64 with one running maximum,
@@ -45,11 +46,13 @@ struct PagedDecodeParams {
   CUtensorMap tm_k;
   CUtensorMap tm_v;
   int row_groups;      // ceil(group * Sq / 16)
+  FastDiv div_rg;      // by row_groups
   int oob_page;        // a page index behind the map's last one (reads as zeros)
   float* part_o;       // [2 * CTAs][16][d] locally normalised partial outputs
   float2* part_ml;     // [2 * CTAs][16] (max of scale * q.k, sum)
-  int4* joins;         // [CTAs] {sequence, head * row_groups + row group, last CTA, -} of the item that
-                       // begins in the CTA's share and ends in a later one; sequence -1: none
+  int4* joins;         // [CTAs] {first token, head * row_groups + row group, last CTA, tokens} of the item
+                       // that begins in the CTA's share and ends in a later one; first token -1: none
+  int64_t lse_tok, lse_head;  // element of the lse: lse_tok * tok0 + lse_head * head + token - tok0
 };
 
 template <int D>
@@ -66,58 +69,107 @@ struct PagedDecodeCfg {
   static_assert(kPdCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of two blocks");
 };
 
-__device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
-  const int64_t cap = static_cast<int64_t>(p.max_pages) << p.page_shift;
-  return static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.lens + b), 0)), cap));
-}
-
-// Tiles of an item over `len` keys; an empty one takes a place as well (its rows are written).
+// Tiles of an item over `len` keys; an empty one takes one as well (its rows are written).
 __device__ __forceinline__ int pd_tiles(int len) { return max(1, (len + kPdKeys - 1) / kPdKeys); }
 
-// Length of an item of sequence b on the line.
-__device__ __forceinline__ int pd_cost(const PagedParams& p, int b) { return pd_tiles(paged_len(p, b)) + kPdItemCost; }
+// The tokens of sequence b: all of the decode's Sq; those of a ragged sequence
+// where they are few (kRowUnit).
+struct PdSeq {
+  int tok0, cnt;  // first token's row of q, tokens (0: no item)
+  int L;          // keys that any of them sees
+  int lim;        // last key that the first token sees (causal)
+  int T;          // tiles of an item, 0 without one
+};
 
-// Barrier of the consumer warps that also tells whether `pred` holds in any thread.
-__device__ __forceinline__ bool pd_any(bool pred) {
+__device__ __forceinline__ PdSeq pd_of(const PagedParams& p, const PagedSeq& q) {
+  PdSeq s;
+  s.tok0 = q.start;
+  s.cnt = q.n <= p.row_tokens ? q.n : 0;
+  s.lim = p.causal == 2 ? q.L - q.n : 0;
+  s.L = paged_visible(p.causal, q.n, q.L, s.lim);
+  s.T = s.cnt > 0 ? pd_tiles(s.L) : 0;
+  return s;
+}
+
+__device__ __forceinline__ PdSeq pd_seq(const PagedParams& p, int b) {
+  if (p.cu_q != nullptr) return pd_of(p, paged_seq(p, b));
+  PdSeq s;
+  s.tok0 = b * p.Sq;
+  s.cnt = p.Sq;
+  s.L = paged_clamp(p, __ldg(p.lens + b));
+  s.lim = p.causal == 2 ? s.L - p.Sq : 0;
+  s.T = pd_tiles(s.L);
+  return s;
+}
+
+// Length of an item on the line.
+__device__ __forceinline__ int pd_cost(const PdSeq& s) { return s.T > 0 ? s.T + kPdItemCost : 0; }
+
+// Barrier `id` of a CTA's consumer warps that also tells whether `pred` holds in any thread.
+__device__ __forceinline__ bool pd_any(int id, bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(pred ? 1u : 0u), "n"(kPdWarps * 32)
+      : "r"(pred ? 1u : 0u), "r"(id), "n"(kPdWarps * 32)
       : "memory");
   return r != 0;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedDecodeParams a) {
-  using Cfg = PagedDecodeCfg<D>;
-  constexpr int NS = Cfg::kStages;
-  const PagedParams& p = a.p;
-  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's pattern repeats every 1024 bytes
-  const uint32_t ring = smem_u32(smem);
-  float* const s_o = reinterpret_cast<float*>(smem + NS * Cfg::kStageBytes);  // [2 warps][16][D]
-  float* const s_m = s_o + kPdWarps / 2 * kPdRows * D;                        // [2][16]
-  float* const s_l = s_m + kPdWarps / 2 * kPdRows;                            // [2][16]
-  const uint32_t bar0 = ring + Cfg::kBarOffset;
-  auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
-  auto seg_full = [&](int s) { return bar0 + 8u * (2 * NS + s); };
-  auto seg_empty = [&](int s) { return bar0 + 8u * (2 * NS + kPdSegRing + s); };
-  // ring of announced pieces: {sequence (-1: no more), head * row_groups + row group, first tile, tiles, keys, slot
-  // of the partial (-1: whole item)}
-  volatile int* const segs = reinterpret_cast<volatile int*>(smem + Cfg::kSegOffset);
-  volatile int* const abort_flag = segs + kPdSegRing * 8;
-  int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + Cfg::kSumOffset);  // [5]
-  int64_t& s_prefix = s_sum[kPdWarps + 1];  // places of the sequences before this CTA's first one, per item
-  int64_t& s_first = s_sum[kPdWarps + 2];   // that sequence
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
+// Token of a KV head's query row.
+__device__ __forceinline__ int row_token(const PagedParams& p, int row) {
+  return static_cast<int>(fastdiv(static_cast<uint32_t>(row), p.div_group));
+}
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
+// Where a share of the line begins and ends.
+struct PdShare {
+  int64_t x0, x1, total;
+  int G;           // shares
+  int64_t prefix;  // places of the sequences before the share's first one, per (head, row group)
+  int first;       // that sequence
+};
+
+__device__ __forceinline__ PdShare pd_share(int64_t total, int ctas, int cta) {
+  PdShare s;
+  // every share has a place at least; with fewer places than CTAs the last CTAs have none
+  s.total = total;
+  s.G = static_cast<int>(min(static_cast<int64_t>(ctas), total));
+  s.x0 = cta < s.G ? div64(total * cta, s.G) : 0;
+  s.x1 = cta < s.G ? div64(total * (cta + 1), s.G) : 0;
+  s.prefix = 0;
+  s.first = 0;
+  return s;
+}
+
+// Shared memory of one CTA's producer and consumers at `smem` (1024-byte aligned: the swizzle's pattern).
+template <int D>
+struct PdSmem {
+  using Cfg = PagedDecodeCfg<D>;
+  uint32_t ring;
+  float *s_o, *s_m, *s_l;  // merge: [2 warps][16][D], [2][16], [2][16]
+  uint32_t bar0;
+  // ring of announced pieces: {first token (-1: no more), head * row_groups + row group, first tile, tiles, keys,
+  // slot of the partial (-1: whole item), tokens, last key the first token sees}
+  volatile int* segs;
+  volatile int* abort_flag;
+  __device__ __forceinline__ explicit PdSmem(uint8_t* smem) {
+    ring = smem_u32(smem);
+    s_o = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes);
+    s_m = s_o + kPdWarps / 2 * kPdRows * D;
+    s_l = s_m + kPdWarps / 2 * kPdRows;
+    bar0 = ring + Cfg::kBarOffset;
+    segs = reinterpret_cast<volatile int*>(smem + Cfg::kSegOffset);
+    abort_flag = segs + kPdSegRing * 8;
+  }
+  __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (Cfg::kStages + s); }
+  __device__ __forceinline__ uint32_t seg_full(int s) const { return bar0 + 8u * (2 * Cfg::kStages + s); }
+  __device__ __forceinline__ uint32_t seg_empty(int s) const { return bar0 + 8u * (2 * Cfg::kStages + kPdSegRing + s); }
+  __device__ __forceinline__ void init() const {  // one thread
+    for (int s = 0; s < Cfg::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), kPdWarps);
     }
@@ -128,209 +180,159 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kPdWarps && lane == 0) {
-    tma_prefetch_desc(&a.tm_k);
-    tma_prefetch_desc(&a.tm_v);
-  }
-  __syncthreads();
-  // Launched as a programmatic dependent of whatever precedes it on the stream:
-  // no global memory is touched before this wait.
-  grid_dependency_wait();
-  grid_dependency_trigger();
+};
 
-  // ---- this CTA's share of the line
-  const int per_seq = p.Hkv * a.row_groups;  // items per sequence
-  const int cta = static_cast<int>(blockIdx.x);
-  int64_t total = 0, x0 = 0, x1 = 0;
-  int G = 0;
-  auto share = [&]() {
-    // every share has a place at least; with fewer places than CTAs the last CTAs have none
-    G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    if (cta < G) {
-      x0 = div64(total * cta, G);
-      x1 = div64(total * (cta + 1), G);
+// The producer warp of share `sh`, which is CTA number `cta` of the line.
+template <int D>
+__device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const PdSmem<D>& sm, const PdShare& sh, int cta,
+                                            int lane) {
+  using Cfg = PagedDecodeCfg<D>;
+  constexpr int NS = Cfg::kStages;
+  const PagedParams& p = a.p;
+  const int per_seq = p.Hkv * a.row_groups;
+  const int pb = min(1 << p.page_shift, kPdKeys);  // rows per copy
+  const int pb_shift = min(p.page_shift, 6);
+  const int nb = kPdKeys >> pb_shift;              // copies per K (or V) tile
+  const uint32_t box_bytes = static_cast<uint32_t>(pb) * D * 2;
+  const bool is_v = lane >= nb;
+  const int box = is_v ? lane - nb : lane;
+  int4 join = make_int4(-1, 0, 0, 0);  // the item that a later share ends
+  int64_t join_end = 0;
+  int issued = 0, nseg = 0;
+  // keys and values are read once (twice with two row groups): what else is in the L2, this kernel's
+  // code among it, is worth more
+  const uint64_t policy = l2_evict_first();
+  bool ok = true;
+  auto announce = [&](const PdSeq& q, int hr, int tile, int n, int slot) {
+    const int k = nseg % kPdSegRing;
+    ok = __all_sync(0xffffffffu, nseg < kPdSegRing ||
+                                     mbar_wait(sm.seg_empty(k), ((nseg / kPdSegRing) - 1) & 1, sm.abort_flag));
+    if (ok && lane == 0) {
+      volatile int* s = sm.segs + 8 * k;
+      s[0] = q.tok0;
+      s[1] = hr;
+      s[2] = tile;
+      s[3] = n;
+      s[4] = q.L;
+      s[5] = slot;
+      s[6] = q.cnt;
+      s[7] = q.lim;
+      mbar_arrive(sm.seg_full(k));
     }
+    ++nseg;
   };
-  // Inclusive sum of t over the block's threads so far, and their total.
-  auto block_scan = [&](int t, int64_t& incl, int64_t& all) {
-    int w_incl = t;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w_incl, off);
-      if (lane >= off) w_incl += u;
-    }
-    if (lane == 31) s_sum[warp] = w_incl;
-    __syncthreads();
-    incl = w_incl;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kPdThreads / 32; ++w) {
-      if (w < warp) incl += s_sum[w];
-      all += s_sum[w];
-    }
-  };
-  auto find = [&](int b, int t, int64_t end) {  // sequence b's places end at `end`
-    if (t > 0 && (end - t) * per_seq <= x0 && x0 < end * per_seq) {
-      s_first = b;
-      s_prefix = end - t;
-    }
-  };
-  if (p.B <= kPdThreads) {
-    const int t = static_cast<int>(threadIdx.x) < p.B ? pd_cost(p, threadIdx.x) : 0;
-    int64_t incl;
-    block_scan(t, incl, total);
-    total *= per_seq;
-    share();
-    find(threadIdx.x, t, incl);
-  } else {
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += kPdThreads) mine += pd_cost(p, b);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPdThreads / 32; ++w) total += s_sum[w];
-    total *= per_seq;
-    share();
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.B && x0 < x1 && base * per_seq <= x0; b0 += kPdThreads) {  // block-uniform
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      const int t = b < p.B ? pd_cost(p, b) : 0;
-      __syncthreads();  // s_sum's previous contents are read
-      int64_t incl, all;
-      block_scan(t, incl, all);
-      find(b, t, base + incl);
-      base += all;
-    }
-  }
-  __syncthreads();
-
-  if (warp == kPdWarps) {
-    // ------------------------------------------------------------ producer
-    const int pb = min(1 << p.page_shift, kPdKeys);  // rows per copy
-    const int pb_shift = min(p.page_shift, 6);
-    const int nb = kPdKeys >> pb_shift;              // copies per K (or V) tile
-    const uint32_t box_bytes = static_cast<uint32_t>(pb) * D * 2;
-    const bool is_v = lane >= nb;
-    const int box = is_v ? lane - nb : lane;
-    int4 join = make_int4(-1, 0, 0, 0);
-    int issued = 0, nseg = 0;
-    bool ok = true;
-    auto announce = [&](int b, int hr, int tile, int n, int L, int slot) {
-      const int k = nseg % kPdSegRing;
-      ok = __all_sync(0xffffffffu, nseg < kPdSegRing ||
-                                       mbar_wait(seg_empty(k), ((nseg / kPdSegRing) - 1) & 1, abort_flag));
-      if (ok && lane == 0) {
-        volatile int* s = segs + 8 * k;
-        s[0] = b;
-        s[1] = hr;
-        s[2] = tile;
-        s[3] = n;
-        s[4] = L;
-        s[5] = slot;
-        mbar_arrive(seg_full(k));
+  if (sh.x0 < sh.x1) {
+    int b = sh.first;
+    PdSeq s = pd_seq(p, b);
+    const int64_t in_seq = sh.x0 - sh.prefix * per_seq;
+    int hr = static_cast<int>(div64(in_seq, s.T + kPdItemCost));
+    // places of the share that lie before the item's end: an item's first kPdItemCost places stand
+    // for its fixed cost, the others for its tiles
+    int64_t xs = sh.prefix * per_seq + static_cast<int64_t>(hr) * (s.T + kPdItemCost);
+    int tile = max(0, static_cast<int>(sh.x0 - xs) - kPdItemCost);
+    // the page of this lane's copy of tile `tl`: a table entry, oob_page when it is none, -1 behind the last key
+    auto page_of = [&](int bb, int tl, int len) -> int {
+      const int key = tl * kPdKeys + (box << pb_shift);
+      if (lane >= 2 * nb || key >= len) return -1;
+      int page = __ldg(p.table + static_cast<int64_t>(bb) * p.max_pages + (key >> p.page_shift));
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(&g_error_word, kErrPage);
+        page = a.oob_page;
       }
-      ++nseg;
+      return page;
     };
-    if (x0 < x1) {
-      int b = static_cast<int>(s_first);
-      int L = paged_len(p, b);
-      int T = pd_tiles(L);
-      const int64_t in_seq = x0 - s_prefix * per_seq;
-      int hr = static_cast<int>(div64(in_seq, T + kPdItemCost));
-      // places of the share that lie before the item's end: an item's first kPdItemCost places stand
-      // for its fixed cost, the others for its tiles
-      int64_t xs = s_prefix * per_seq + static_cast<int64_t>(hr) * (T + kPdItemCost);
-      int tile = max(0, static_cast<int>(x0 - xs) - kPdItemCost);
-      // the page of this lane's copy of tile `tl`: a table entry, oob_page when it is none, -1 behind the last key
-      auto page_of = [&](int bb, int tl, int len) -> int {
-        const int key = tl * kPdKeys + (box << pb_shift);
-        if (lane >= 2 * nb || key >= len) return -1;
-        int page = __ldg(p.table + static_cast<int64_t>(bb) * p.max_pages + (key >> p.page_shift));
-        if (page < 0 || page >= p.num_pages) {
-          atomicOr(&g_error_word, kErrPage);
-          page = a.oob_page;
+    int page = page_of(b, tile, s.L);
+    while (ok && xs + kPdItemCost < sh.x1) {
+      // a piece: tiles tile .. of item (b, hr), to its end or the share's
+      const int n = static_cast<int>(min(static_cast<int64_t>(s.T), sh.x1 - xs - kPdItemCost)) - tile;
+      const bool whole = tile == 0 && n == s.T;
+      const int head = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_rg));
+      {
+        // the piece's query rows into the first-level cache
+        const int r0 = (hr - head * a.row_groups) * kPdRows;
+        constexpr int kLines = D * 2 / 128;
+        const int r = r0 + lane / kLines;
+        if (lane < kPdRows * kLines && r < p.group * s.cnt) {
+          const int i = row_token(p, r);
+          prefetch_l1(p.q + (static_cast<int64_t>(s.tok0 + i) * p.Hq + head * p.group + r - i * p.group) * D +
+                      (lane % kLines) * 64);
         }
-        return page;
-      };
-      int page = page_of(b, tile, L);
-      while (ok && xs + kPdItemCost < x1) {
-        // a piece: tiles tile .. of item (b, hr), to its end or the share's
-        const int n = static_cast<int>(min(static_cast<int64_t>(T), x1 - xs - kPdItemCost)) - tile;
-        const bool whole = tile == 0 && n == T;
-        const int head = hr / a.row_groups;
-        {
-          // the piece's query rows into the first-level cache (rows of a token are contiguous)
-          const int r0 = (hr - head * a.row_groups) * kPdRows;
-          const int lines = D * 2 / 128;
-          const int r = r0 + lane / lines;
-          if (lane < kPdRows * lines && r < p.group * p.Sq) {
-            const int i = r / p.group;
-            prefetch_l1(p.q + ((static_cast<int64_t>(b) * p.Sq + i) * p.Hq + head * p.group + r - i * p.group) * D +
-                        (lane % lines) * 64);
-          }
-        }
-        if (tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != L) atomicOr(&g_error_word, kErrSeqlen);
-        if (tile == 0 && n < T) {
-          const int64_t last = xs + kPdItemCost + T;  // the CTA whose share holds the item's last tile
-          join = make_int4(b, hr, static_cast<int>(div64(last * G - 1, total)), 0);
-        }
-        const int nk = L > 0 ? n : 0;
-        announce(b, hr, tile, nk, L, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
-        const int64_t xe = xs + kPdItemCost + T;
-        const bool more = xe + kPdItemCost < x1;  // the next item has tiles in this share
-        int nb2 = b, nhr = hr + 1, nL = L, nT = T;
-        if (nhr == per_seq) {
-          nhr = 0;
-          nb2 = b + 1;
-          if (more) {
-            nL = paged_len(p, nb2);
-            nT = pd_tiles(nL);
-          }
-        }
-        for (int i = 0; ok && i < nk; ++i) {
-          const int tl = tile + i;
-          const int cur = page;
-          if (i + 1 < nk) page = page_of(b, tl + 1, L);
-          else if (more) page = page_of(nb2, 0, nL);
-          const int st = issued % NS;
-          ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((issued / NS) & 1) ^ 1, abort_flag));
-          if (!ok) break;
-          const int copies = min(nb, (L - tl * kPdKeys + pb - 1) >> pb_shift);
-          if (lane == 0) mbar_arrive_expect_tx(full(st), 2u * static_cast<uint32_t>(copies) * box_bytes);
-          __syncwarp();
-          if (cur >= 0) {
-            const int row = (tl * kPdKeys + (box << pb_shift)) & ((1 << p.page_shift) - 1);
-            tma_load_5d(ring + st * Cfg::kStageBytes + (is_v ? Cfg::kHalfBytes : 0) + box * box_bytes,
-                        is_v ? &a.tm_v : &a.tm_k, 0, row, 0, head, cur, full(st));
-          }
-          ++issued;
-        }
-        if (nk == 0 && more) page = page_of(nb2, 0, nL);
-        xs = xe;
-        b = nb2;
-        hr = nhr;
-        L = nL;
-        T = nT;
-        tile = 0;
       }
+      if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != s.L)
+        atomicOr(&g_error_word, kErrSeqlen);
+      if (tile == 0 && n < s.T) {
+        join = make_int4(s.tok0, hr, 0, s.cnt);
+        join_end = xs + kPdItemCost + s.T;
+      }
+      const int nk = s.L > 0 ? n : 0;
+      announce(s, hr, tile, nk, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
+      const int64_t xe = xs + kPdItemCost + s.T;
+      const bool more = xe + kPdItemCost < sh.x1;  // the next item has tiles in this share
+      int nb2 = b, nhr = hr + 1;
+      PdSeq ns = s;
+      if (nhr == per_seq) {
+        nhr = 0;
+        if (more) {
+          if (p.cu_q == nullptr) {
+            ++nb2;
+          } else {  // the next sequence with an item
+            unsigned some = 0u;
+            for (++nb2; nb2 < p.B && some == 0u; nb2 += 32) {
+              some = __ballot_sync(0xffffffffu, nb2 + lane < p.B && pd_seq(p, nb2 + lane).cnt > 0);
+              if (some != 0u) nb2 += __ffs(some) - 1 - 32;
+            }
+            if (some == 0u) break;
+          }
+          ns = pd_seq(p, nb2);
+        }
+      }
+      for (int i = 0; ok && i < nk; ++i) {
+        const int tl = tile + i;
+        const int cur = page;
+        if (i + 1 < nk) page = page_of(b, tl + 1, s.L);
+        else if (more) page = page_of(nb2, 0, ns.L);
+        const int st = issued % NS;
+        ok = __all_sync(0xffffffffu, mbar_wait(sm.empty(st), ((issued / NS) & 1) ^ 1, sm.abort_flag));
+        if (!ok) break;
+        const int copies = min(nb, (s.L - tl * kPdKeys + pb - 1) >> pb_shift);
+        if (lane == 0) mbar_arrive_expect_tx(sm.full(st), 2u * static_cast<uint32_t>(copies) * box_bytes);
+        __syncwarp();
+        if (cur >= 0) {
+          const int row = (tl * kPdKeys + (box << pb_shift)) & ((1 << p.page_shift) - 1);
+          tma_load_5d_hint(sm.ring + st * Cfg::kStageBytes + (is_v ? Cfg::kHalfBytes : 0) + box * box_bytes,
+                      is_v ? &a.tm_v : &a.tm_k, 0, row, 0, head, cur, sm.full(st), policy);
+        }
+        ++issued;
+      }
+      if (nk == 0 && more) page = page_of(nb2, 0, ns.L);
+      xs = xe;
+      b = nb2;
+      hr = nhr;
+      s = ns;
+      tile = 0;
     }
-    if (lane == 0) a.joins[cta] = join;
-    if (ok) announce(-1, 0, 0, 0, 0, 0);
-    // copies still in flight must land before the CTA may exit
-    if (lane == 0)
-      for (int it = max(0, issued - NS); it < issued; ++it) mbar_wait_drain(full(it % NS), (it / NS) & 1);
-    __syncwarp();
-    return;
   }
+  // the CTA whose share holds its last tile
+  if (join.x >= 0) join.z = static_cast<int>(div64(join_end * sh.G - 1, sh.total));
+  if (lane == 0) a.joins[cta] = join;
+  if (ok) announce(PdSeq{-1, 0, 0, 0, 0}, 0, 0, 0, 0);
+  // copies still in flight must land before the CTA may exit
+  if (lane == 0)
+    for (int it = max(0, issued - NS); it < issued; ++it) mbar_wait_drain(sm.full(it % NS), (it / NS) & 1);
+  __syncwarp();
+}
 
-  // ------------------------------------------------------------ consumers
+// A consumer warp (0 .. 3); the four meet at named barrier `bar`.
+template <int D>
+__device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const PdSmem<D>& sm, int warp, int lane, int bar) {
+  using Cfg = PagedDecodeCfg<D>;
+  constexpr int NS = Cfg::kStages;
+  const PagedParams& p = a.p;
+  const int tid = warp * 32 + lane;
   const float c = p.scale_log2;
   const int kb = warp * 16;            // this warp's 16 keys of a tile
   const int qr = lane >> 2;            // fragment row (and row + 8)
   const int qc = (lane & 3) * 2;       // fragment column pair
-  const int rows_total = p.group * p.Sq;
   const int pb_shift = min(p.page_shift, 6);
   const uint32_t blk_bytes = 128u << pb_shift;          // one 64-column block of a copy
   const uint32_t box_bytes = blk_bytes * (D / 64);
@@ -349,25 +351,27 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
   int it0 = 0;  // tiles of the CTA's earlier pieces
   for (int sg = 0;; ++sg) {
     const int sk = sg % kPdSegRing;
-    bool ok = __all_sync(0xffffffffu, mbar_wait(seg_full(sk), (sg / kPdSegRing) & 1, abort_flag));
-    int b = -1, hr = 0, tile0 = 0, n = 0, L = 0;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(sm.seg_full(sk), (sg / kPdSegRing) & 1, sm.abort_flag));
+    int tok0 = -1, hr = 0, tile0 = 0, n = 0, L = 0, cnt = 0, lim0 = 0;
     if (ok) {
-      volatile int* s = segs + 8 * sk;
-      b = s[0];
+      volatile int* s = sm.segs + 8 * sk;
+      tok0 = s[0];
       hr = s[1];
       tile0 = s[2];
       n = s[3];
       L = s[4];
+      cnt = s[6];
+      lim0 = s[7];
     }
-    int head = hr / a.row_groups;
+    int head = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_rg));
     int row0 = (hr - head * a.row_groups) * kPdRows;  // first of the head's query rows
-    const int rows = min(kPdRows, rows_total - row0);
+    const int rows = min(kPdRows, p.group * cnt - row0);
     float o[D / 8][4];
 #pragma unroll
     for (int e = 0; e < D / 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY};
     float l[2] = {0.f, 0.f};
-    if (ok && b >= 0 && n > 0) {
+    if (ok && tok0 >= 0 && n > 0) {
       // query row r of the head: token r / group, head r mod group
       uint32_t qf[D / 16][4];
       int lim[2];  // last key that rows qr and qr + 8 see
@@ -375,12 +379,12 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       for (int h = 0; h < 2; ++h) {
         const int r = qr + 8 * h;
         const bool live = r < rows;
-        const int i = live ? (row0 + r) / p.group : 0;
+        const int i = live ? row_token(p, row0 + r) : 0;
         const int g = live ? row0 + r - i * p.group : 0;
         lim[h] = L - 1;
-        if (p.causal && live) lim[h] = min(lim[h], p.causal == 2 ? L - p.Sq + i : i);
+        if (p.causal && live) lim[h] = min(lim[h], lim0 + i);
         const uint32_t* q = reinterpret_cast<const uint32_t*>(
-            p.q + ((static_cast<int64_t>(b) * p.Sq + i) * p.Hq + head * p.group + g) * D);
+            p.q + (static_cast<int64_t>(tok0 + i) * p.Hq + head * p.group + g) * D);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           qf[ks][h] = live ? __ldg(q + ((ks * 16 + qc) >> 1)) : 0u;
@@ -390,12 +394,12 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       for (int i = 0; i < n; ++i) {
         const int it = it0 + i;
         const int st = it % NS;
-        if (!__all_sync(0xffffffffu, mbar_wait(full(st), (it / NS) & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(sm.full(st), (it / NS) & 1, sm.abort_flag))) {
           ok = false;
           break;
         }
-        const uint32_t sK = ring + st * Cfg::kStageBytes + k_base;
-        const uint32_t sV = ring + st * Cfg::kStageBytes + Cfg::kHalfBytes + v_base;
+        const uint32_t sK = sm.ring + st * Cfg::kStageBytes + k_base;
+        const uint32_t sV = sm.ring + st * Cfg::kStageBytes + Cfg::kHalfBytes + v_base;
         const int key0 = (tile0 + i) * kPdKeys + kb;
         if (key0 < L) {  // warp-uniform
           float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(st));
+        if (lane == 0) mbar_arrive(sm.empty(st));
       }
       it0 += n;
 #pragma unroll
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
     const int mw = warp & 1;
     int x = qr;
     asm volatile("" : "+r"(x));  // the offsets below are not to be held in registers over the tiles
-    const uint32_t part = smem_u32(s_o) + ((mw * kPdRows + x) * D + qc) * 4;  // row qr's column qc of eight 0
+    const uint32_t part = smem_u32(sm.s_o) + ((mw * kPdRows + x) * D + qc) * 4;  // row qr's column qc of eight 0
     auto leave = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -499,21 +503,21 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
           for (int e = 0; e < D / 8; ++e)
             st_shared_f2(part + h * (8 * D * 4) + (e & ~3) * 32 + (((e ^ x) & 3) << 5), o[e][2 * h], o[e][2 * h + 1]);
           if ((lane & 3) == 0) {
-            s_m[mw * kPdRows + r] = m[h];
-            s_l[mw * kPdRows + r] = l[h];
+            sm.s_m[mw * kPdRows + r] = m[h];
+            sm.s_l[mw * kPdRows + r] = l[h];
           }
         }
       }
     };
     if (n > 0 && warp >= 2) leave();
     // every consumer meets here once per piece, and all of them leave together
-    if (pd_any(!ok) || b < 0) break;
+    if (pd_any(bar, !ok) || tok0 < 0) break;
     if (n > 0 && warp < 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = qr + 8 * h;
         if (r < rows) {
-          const float m1 = s_m[mw * kPdRows + r], l1 = s_l[mw * kPdRows + r];
+          const float m1 = sm.s_m[mw * kPdRows + r], l1 = sm.s_l[mw * kPdRows + r];
           const float M = fmaxf(l[h] > 0.f ? m[h] : -INFINITY, l1 > 0.f ? m1 : -INFINITY);
           const float w0 = l[h] > 0.f ? ex2_approx((m[h] - M) * c) : 0.f;
           const float w1 = l1 > 0.f ? ex2_approx((m1 - M) * c) : 0.f;
@@ -530,20 +534,20 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       __syncwarp();  // the warp has read the rows it now overwrites
       leave();
     }
-    named_bar_sync(1, kPdWarps * 32);
+    named_bar_sync(bar, kPdWarps * 32);
     // the announced piece again: it need not stay in registers over the tiles
-    b = segs[8 * sk];
-    hr = segs[8 * sk + 1];
-    const int slot = segs[8 * sk + 5];
-    head = hr / a.row_groups;
+    tok0 = sm.segs[8 * sk];
+    hr = sm.segs[8 * sk + 1];
+    const int slot = sm.segs[8 * sk + 5];
+    head = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_rg));
     row0 = (hr - head * a.row_groups) * kPdRows;
     __syncwarp();
-    if (lane == 0) mbar_arrive(seg_empty(sk));
+    if (lane == 0) mbar_arrive(sm.seg_empty(sk));
     // 8 threads per row, D/8 consecutive columns each
-    const int r = static_cast<int>(threadIdx.x) >> 3;
+    const int r = tid >> 3;
     if (r < rows) {
       constexpr int kCols = D / 8;
-      const int c0 = (static_cast<int>(threadIdx.x) & 7) * kCols;
+      const int c0 = (tid & 7) * kCols;
       float M = -INFINITY, sum = 0.f;
       float wt[kPdWarps / 2];
       float acc[kCols];
@@ -552,18 +556,18 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       if (n > 0) {
 #pragma unroll
         for (int w = 0; w < kPdWarps / 2; ++w)
-          if (s_l[w * kPdRows + r] > 0.f) M = fmaxf(M, s_m[w * kPdRows + r]);
+          if (sm.s_l[w * kPdRows + r] > 0.f) M = fmaxf(M, sm.s_m[w * kPdRows + r]);
 #pragma unroll
         for (int w = 0; w < kPdWarps / 2; ++w) {
-          const float lw = s_l[w * kPdRows + r];
-          wt[w] = lw > 0.f ? ex2_approx((s_m[w * kPdRows + r] - M) * c) : 0.f;
+          const float lw = sm.s_l[w * kPdRows + r];
+          wt[w] = lw > 0.f ? ex2_approx((sm.s_m[w * kPdRows + r] - M) * c) : 0.f;
           sum += wt[w] * lw;
         }
 #pragma unroll
         for (int w = 0; w < kPdWarps / 2; ++w)
 #pragma unroll
           for (int e = 0; e < kCols; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * kPdRows + r) * D + ((c0 + e) ^ ((r & 3) * 8))]);
+            const float4 v = *reinterpret_cast<const float4*>(&sm.s_o[(w * kPdRows + r) * D + ((c0 + e) ^ ((r & 3) * 8))]);
             acc[e] += wt[w] * v.x;
             acc[e + 1] += wt[w] * v.y;
             acc[e + 2] += wt[w] * v.z;
@@ -572,15 +576,15 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
       }
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       if (slot < 0) {
-        const int i = (row0 + r) / p.group;
+        const int i = row_token(p, row0 + r);
         const int hq = head * p.group + row0 + r - i * p.group;
-        uint16_t* const dst = p.o + ((static_cast<int64_t>(b) * p.Sq + i) * p.Hq + hq) * D + c0;
+        uint16_t* const dst = p.o + (static_cast<int64_t>(tok0 + i) * p.Hq + hq) * D + c0;
 #pragma unroll
         for (int e = 0; e < kCols; e += 4)
           *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv),
                                                           pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
         if (c0 == 0 && p.lse != nullptr)
-          p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + i] =
+          p.lse[a.lse_tok * tok0 + a.lse_head * hq + i] =
               sum > 0.f ? M * p.scale + lg2_approx(sum) * 0.69314718055994531f : -INFINITY;
       } else {
         float* const dst = a.part_o + (static_cast<int64_t>(slot) * kPdRows + r) * D + c0;
@@ -591,8 +595,98 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
         if (c0 == 0) a.part_ml[slot * kPdRows + r] = make_float2(sum > 0.f ? M * p.scale : -INFINITY, sum);
       }
     }
-    named_bar_sync(1, kPdWarps * 32);  // the merge buffer is read
+    named_bar_sync(bar, kPdWarps * 32);  // the merge buffer is read
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(const __grid_constant__ PagedDecodeParams a) {
+  using Cfg = PagedDecodeCfg<D>;
+  const PagedParams& p = a.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const PdSmem<D> sm(smem);
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + Cfg::kSumOffset);  // [5]
+  int64_t& s_prefix = s_sum[kPdWarps + 1];
+  int64_t& s_first = s_sum[kPdWarps + 2];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) sm.init();
+  if (warp == kPdWarps && lane == 0) {
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+  }
+  __syncthreads();
+  // Launched as a programmatic dependent of whatever precedes it on the stream:
+  // no global memory is touched before this wait.
+  grid_dependency_wait();
+  grid_dependency_trigger();
+
+  // ---- this CTA's share of the line
+  const int per_seq = p.Hkv * a.row_groups;  // items per sequence
+  const int cta = static_cast<int>(blockIdx.x);
+  const int ctas = static_cast<int>(gridDim.x);
+  int64_t total = 0;
+  PdShare sh;
+  // Inclusive sum of t over the block's threads so far, and their total.
+  auto block_scan = [&](int t, int64_t& incl, int64_t& all) {
+    int w_incl = t;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w_incl, off);
+      if (lane >= off) w_incl += u;
+    }
+    if (lane == 31) s_sum[warp] = w_incl;
+    __syncthreads();
+    incl = w_incl;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kPdThreads / 32; ++w) {
+      if (w < warp) incl += s_sum[w];
+      all += s_sum[w];
+    }
+  };
+  auto find = [&](int b, int t, int64_t end) {  // sequence b's places end at `end`
+    if (t > 0 && (end - t) * per_seq <= sh.x0 && sh.x0 < end * per_seq) {
+      s_first = b;
+      s_prefix = end - t;
+    }
+  };
+  if (p.B <= kPdThreads) {
+    const int t = static_cast<int>(threadIdx.x) < p.B ? pd_cost(pd_seq(p, threadIdx.x)) : 0;
+    int64_t incl;
+    block_scan(t, incl, total);
+    total *= per_seq;
+    sh = pd_share(total, ctas, cta);
+    find(threadIdx.x, t, incl);
+  } else {
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += kPdThreads) mine += pd_cost(pd_seq(p, b));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPdThreads / 32; ++w) total += s_sum[w];
+    total *= per_seq;
+    sh = pd_share(total, ctas, cta);
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B && sh.x0 < sh.x1 && base * per_seq <= sh.x0; b0 += kPdThreads) {  // block-uniform
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      const int t = b < p.B ? pd_cost(pd_seq(p, b)) : 0;
+      __syncthreads();  // s_sum's previous contents are read
+      int64_t incl, all;
+      block_scan(t, incl, all);
+      find(b, t, base + incl);
+      base += all;
+    }
+  }
+  __syncthreads();
+
+  sh.first = static_cast<int>(s_first);
+  sh.prefix = s_prefix;
+  if (warp == kPdWarps) pd_producer<D>(a, sm, sh, cta, lane);
+  else pd_consumer<D>(a, sm, warp, lane, 1);
 }
 
 // Join the partial rows of the items that cross shares: block c takes the item
@@ -604,12 +698,10 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
 constexpr int kJoinRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const __grid_constant__ PagedDecodeParams a) {
+__device__ __forceinline__ void paged_decode_join(const PagedDecodeParams& a, int cta, int ctas) {
   constexpr int kPer = D / 32;
   constexpr float kLog2e = 1.4426950408889634f;
   const PagedParams& p = a.p;
-  grid_dependency_trigger();
-  const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
   const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // piece 0 lies in CTA cta's slot for the item it begins, piece s in CTA cta + s's for the one it continues
   auto slot_row = [&](int s) { return (2 * min(cta + s, ctas - 1) + (s == 0 ? 1 : 0)) * kPdRows + r; };
@@ -622,16 +714,15 @@ __global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const _
       x[e + 1] = t.y;
     }
   };
-  grid_dependency_wait();
   const int4 join = a.joins[cta];
   float2 ml = a.part_ml[slot_row(lane)];
   float x[kJoinRows][kPer];
 #pragma unroll
   for (int u = 0; u < kJoinRows; ++u) load(u, x[u]);
   if (join.x < 0) return;
-  const int head = join.y / a.row_groups;
+  const int head = static_cast<int>(fastdiv(static_cast<uint32_t>(join.y), a.div_rg));
   const int row = (join.y - head * a.row_groups) * kPdRows + r;  // of the head's query rows
-  if (row >= p.group * p.Sq) return;
+  if (row >= p.group * join.w) return;
   const int pieces = join.z - cta + 1;
   float M = -INFINITY;
   for (int s0 = 0; s0 < pieces; s0 += 32) {
@@ -667,15 +758,22 @@ __global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const _
     }
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
-  const int i = row / p.group;
+  const int i = row_token(p, row);
   const int hq = head * p.group + row - i * p.group;
-  uint16_t* const dst = p.o + ((static_cast<int64_t>(join.x) * p.Sq + i) * p.Hq + hq) * D + lane * kPer;
+  uint16_t* const dst = p.o + (static_cast<int64_t>(join.x + i) * p.Hq + hq) * D + lane * kPer;
 #pragma unroll
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(join.x) * p.Hq + hq) * p.Sq + i] =
+    p.lse[a.lse_tok * join.x + a.lse_head * hq + i] =
         W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPdRows * 32) paged_decode_join_kernel(const __grid_constant__ PagedDecodeParams a) {
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  paged_decode_join<D>(a, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 }  // namespace sdpa

@@ -10,11 +10,11 @@
 //     fits).  K/V are loaded once for the whole group, and a chunk of n tokens
 //     fills its tiles with n * hc rows: 32 tokens of 4 heads are a full tile.
 //   * A unit is two such tiles that share every K/V tile.  A unit with rows in
-//     one tile only (a single token, a chunk's end) is thin: both tiles hold
+//     one tile only (a chunk's end) is thin: both tiles hold
 //     the same rows and take key tiles in turn, so the two softmax chains still
 //     overlap, and the unit's two results are merged in the epilogue (the
 //     second one's output is read from its own TMEM columns).
-//   * All units' keys form one line, in the order (sequence, KV head, unit), cut
+//   * All units' keys form a line, in the order (sequence, KV head, unit), cut
 //     into equal shares, one per CTA (one CTA per SM); a share may begin and end
 //     inside a unit.  A key's weight depends on the unit's kind, and a
 //     unit has a fixed weight besides.  A unit's visible keys are linear in its index, so
@@ -22,6 +22,11 @@
 //     place from the lengths on the device.  A unit that crosses shares leaves
 //     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
 //     programmatic dependent, joins in share order.
+//   * Sequences of no more than kRowUnit rows (a single token of up to 16 heads)
+//     are the decode's work: a 128-row tile would load the same bytes at a lower
+//     rate.  They form a line of their own, and the grid's last CTAs, in the
+//     proportion of the two lines' times, each run as two of the decode kernel's
+//     CTAs (paged_decode.cuh): the bytes stream while the other SMs multiply.
 //   * K/V tiles of 128 keys arrive as one TMA copy per page (or 128 rows of it)
 //     and 64 columns; the producer's lanes issue them side by side, each with
 //     the table entry it read one tile ahead.  Keys behind the last page read as
@@ -29,16 +34,17 @@
 //     the last key hold anything, and 0 times infinity or NaN is NaN, so warp 11
 //     zeroes them in V's last tile before the MMAs may read it.
 #pragma once
-#include "paged.cuh"
+#include "paged_decode.cuh"
 #include "prefill.cuh"
 
 namespace sdpa {
 
 // Weights on the line.  A step of 128 keys takes 2.1 us in a pair (both softmax
-// chains) and 1.6 to 1.9 us per tile in a thin unit (bound by the bytes that its
-// ring keeps in flight); a unit costs 2.4 us besides (first S, last P.V, stores).
-constexpr int kPfPair = 4, kPfThin = 3;   // per key
-constexpr int kPfUnitCost = 576;
+// chains) and 1.7 us per tile in a thin unit (bound by the bytes that its
+// ring keeps in flight); a unit costs 2.8 us besides (first S, last P.V, stores).
+constexpr int kPfPair = 8, kPfThin = 6;   // per key
+constexpr int kPfUnitCost = 1400;
+constexpr float kPfRowPlace = 150.f;      // a place on the short sequences' line: 0.4 us of an SM
 // Units of this many key tiles or fewer are not split: joining costs more.
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
@@ -52,7 +58,7 @@ struct PagedFwdParams {
   int oob_page;       // a page index behind the map's last one (reads as zeros)
   int hc, chunks;     // heads per tile, tiles of heads per group
   int tpt;            // tokens per tile: 128 / hc
-  FastDiv div_hc;
+  FastDiv div_hc, div_tu, div_chunks;  // by hc, 2 tpt, chunks
   float* part_o;      // [2 * CTAs][2 tiles][d][128 rows] locally normalised partial outputs
   float2* part_ml;    // [2 * CTAs][2 tiles][128] (max of scale * q.k, sum)
   int4* joins;        // [CTAs][2] {first token, first head, heads, last CTA (-1: no join)}, {tokens of tile 0, 1, -, -}
@@ -68,9 +74,12 @@ struct PagedFwdCfg {
   static constexpr int kNumBars = 4 + 2 * NS + 8 + 1 + 2 * kPfRing + 2 + NS;
   static constexpr int kRingOffset = (kNumBars * 8 + 15) / 16 * 16;   // pieces: kPfRing x 16 ints
   static constexpr int kMergeOffset = kRingOffset + kPfRing * 64;     // thin units: (max, sum) of tile 1's rows
-  static constexpr int kSumOffset = kMergeOffset + 128 * 8;           // 12 sums, prefix, first sequence
-  static constexpr int kMiscOffset = kSumOffset + 14 * 8;             // TMEM base, abort flag
-  static constexpr int kSmemBytes = (2 + NS) * kTileBytes + kMiscOffset + 8;
+  static constexpr int kEnd = (2 + NS) * kTileBytes + kMergeOffset + 128 * 8;
+  // a CTA that takes short sequences holds two of the decode's CTAs instead
+  static constexpr int kRowsBytes = (PagedDecodeCfg<D>::kSumOffset + 1023) / 1024 * 1024;
+  // above both: sums of 12 warps and two lines, prefix and first sequence of two shares, TMEM base, abort flag
+  static constexpr int kSumOffset = kEnd > 2 * kRowsBytes ? kEnd : 2 * kRowsBytes;
+  static constexpr int kSmemBytes = kSumOffset + 28 * 8 + 8;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 };
 
@@ -78,48 +87,46 @@ struct PagedFwdCfg {
 struct PfSeq {
   int start, n;     // first token, tokens
   int L, coff;      // keys; token i sees key j iff j <= i + coff (causal)
-  int full, units;  // units whose two tiles are full, units
+  int full, units;  // units whose two tiles are full, units (none in a short sequence)
   int64_t cost;     // weight of its units for one (KV head, head tile)
 };
 
-__device__ __forceinline__ int pf_visible(int causal, int64_t tokens, int L, int coff) {
-  return causal ? static_cast<int>(min(max(tokens + coff, int64_t{0}), static_cast<int64_t>(L))) : L;
-}
-
-// Weight of the first V full units (tu tokens each): V times the fixed weight
+// Weight of a sequence's first V full units (tu tokens each): V times the fixed weight
 // and kPfPair times the visible keys, which are clamp((v + 1) tu + coff, 0, L) in unit v.
-__device__ __forceinline__ int64_t pf_prefix(int causal, int V, int tu, int L, int coff) {
+__device__ __forceinline__ int64_t pf_prefix(const PagedFwdParams& a, int V, int L, int coff) {
   const int64_t fixed = static_cast<int64_t>(V) * kPfUnitCost;
-  if (!causal) return fixed + kPfPair * static_cast<int64_t>(V) * L;
-  const int lo = min(V, max(-coff, 0) / tu);                     // units that see nothing
-  const int hi = min(V, max(lo, (L - coff + tu - 1) / tu - 1));  // first unit that sees every key
+  if (!a.p.causal || V == 0) return fixed + kPfPair * static_cast<int64_t>(V) * L;
+  const int tu = 2 * a.tpt;
+  auto div = [&](int x) { return static_cast<int>(fastdiv(static_cast<uint32_t>(x), a.div_tu)); };
+  const int lo = min(V, div(max(-coff, 0)));                     // units that see nothing
+  const int hi = min(V, max(lo, div(L - coff + tu - 1) - 1));    // first unit that sees every key
   const int64_t m = hi - lo;
   const int64_t mid = m * coff + tu * (static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2;
   return fixed + kPfPair * (mid + static_cast<int64_t>(V - hi) * L);
 }
 
-__device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b, bool report) {
+__device__ __forceinline__ PfSeq pf_of(const PagedFwdParams& a, const PagedSeq& q) {
   const PagedParams& p = a.p;
   PfSeq s;
-  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), raw = __ldg(p.lens + b);
-  s.start = min(max(c0, 0), p.T);
-  const int end = min(max(c1, s.start), p.T);
-  s.n = end - s.start;
-  s.L = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), static_cast<int64_t>(p.max_pages) << p.page_shift));
-  if (report && (s.start != c0 || end != c1 || s.L != raw)) atomicOr(&g_error_word, kErrSeqlen);
+  s.start = q.start;
+  s.n = q.n;
+  s.L = q.L;
   s.coff = p.causal == 2 ? s.L - s.n : 0;
-  const int tu = 2 * a.tpt;
-  s.full = s.n / tu;
-  const int rem = s.n - s.full * tu;
-  s.units = s.full + (rem > 0 ? 1 : 0);
-  s.cost = pf_prefix(p.causal, s.full, tu, s.L, s.coff);
-  if (rem > 0)
-    s.cost += kPfUnitCost + (rem > a.tpt ? kPfPair : kPfThin) * static_cast<int64_t>(pf_visible(p.causal, s.n, s.L, s.coff));
+  s.full = static_cast<int>(fastdiv(static_cast<uint32_t>(s.n), a.div_tu));
+  const int rem = s.n - s.full * 2 * a.tpt;
+  const bool more = rem > 0 && s.n > p.row_tokens;
+  s.units = s.full + (more ? 1 : 0);
+  s.cost = pf_prefix(a, s.full, s.L, s.coff);
+  if (more)
+    s.cost += kPfUnitCost + (rem > a.tpt ? kPfPair : kPfThin) * static_cast<int64_t>(paged_visible(p.causal, s.n, s.L, s.coff));
   return s;
 }
 
+__device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b) { return pf_of(a, paged_seq(a.p, b)); }
+
 template <int D, int NS>
-__global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __grid_constant__ PagedFwdParams a) {
+__global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __grid_constant__ PagedFwdParams a,
+                                                                       const __grid_constant__ PagedDecodeParams rows) {
   using Cfg = PagedFwdCfg<D, NS>;
   const PagedParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's pattern repeats every 1024 bytes
@@ -145,10 +152,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   uint8_t* const misc = smem + (2 + NS) * Cfg::kTileBytes;
   volatile int* const ring = reinterpret_cast<volatile int*>(misc + Cfg::kRingOffset);
   float2* const merge_ml = reinterpret_cast<float2*>(misc + Cfg::kMergeOffset);
-  int64_t* const s_sum = reinterpret_cast<int64_t*>(misc + Cfg::kSumOffset);
-  int64_t& s_prefix = s_sum[12];  // weight of the sequences before this CTA's first one, per (KV head, head tile)
-  int64_t& s_first = s_sum[13];   // that sequence
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc + Cfg::kMiscOffset);
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + Cfg::kSumOffset);  // [2 lines][12 warps]
+  int64_t* const s_prefix = s_sum + 24;  // [2 shares] weight of the sequences before the first one, per head
+  int64_t* const s_first = s_sum + 26;   // [2 shares] that sequence
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_sum + 28);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // Entries of an announced piece.
   enum { kHead, kG0, kHeads, kTok0, kCnt0, kCnt1, kLim, kKeys, kJ0, kN0, kN1, kThin, kSlot, kSteps };
@@ -210,36 +217,68 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   grid_dependency_wait();
   grid_dependency_trigger();
 
-  // ---- this CTA's share of the line
-  const int cta = static_cast<int>(blockIdx.x);
-  const int per_seq = p.Hkv * a.chunks;
+  // ---- the two lines, and this CTA's share of one of them
+  const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+  const int per_seq = p.Hkv * a.chunks;  // units' heads; the short sequences have p.Hkv
   int64_t x0 = 0, x1 = 0, total = 0, quot = 0;
   int G = 0, rem = 0;
   auto share_begin = [&](int c) -> int64_t { return quot * c + rem * c / G; };  // floor(total * c / G)
+  int row_ctas = 0;     // the last CTAs of the grid, which take the short sequences
+  bool takes_rows = false;
+  PdShare sh[2];
   {
     constexpr int kWarps = kPrefillThreads / 32;
-    auto cost_of = [&](int b) -> int64_t { return b < p.B ? pf_seq(a, b, cta == 0).cost : 0; };
-    // inclusive sum over the block's threads and their total
-    auto block_scan = [&](int64_t t, int64_t& incl, int64_t& all) {
-      incl = t;
+    auto costs_of = [&](int b, int64_t (&t)[2]) {
+      t[0] = t[1] = 0;
+      if (b >= p.B) return;
+      const PagedSeq q = paged_seq(p, b);
+      if (q.bad && cta == 0) atomicOr(&g_error_word, kErrSeqlen);
+      if (q.n == 0) return;
+      t[0] = pf_of(a, q).cost;
+      t[1] = pd_cost(pd_of(p, q));
+    };
+    // inclusive sums over the block's threads and their totals
+    auto block_scan = [&](const int64_t (&t)[2], int64_t (&incl)[2], int64_t (&all)[2]) {
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += u;
+      for (int q = 0; q < 2; ++q) {
+        incl[q] = t[q];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, incl[q], off);
+          if (lane >= off) incl[q] += u;
+        }
+        if (lane == 31) s_sum[q * kWarps + warp] = incl[q];
       }
-      if (lane == 31) s_sum[warp] = incl;
       __syncthreads();
-      all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) incl += s_sum[w];
-        all += s_sum[w];
+      for (int q = 0; q < 2; ++q) {
+        all[q] = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) incl[q] += s_sum[q * kWarps + w];
+          all[q] += s_sum[q * kWarps + w];
+        }
       }
     };
-    auto share = [&]() {
+    auto share = [&](const int64_t (&all)[2]) {
+      total = all[0] * per_seq;
+      const int64_t row_total = all[1] * p.Hkv;
+      // CTAs for the short sequences: in proportion to the two lines' times
+      if (row_total > 0) {
+        const float wr = static_cast<float>(row_total) * kPfRowPlace, wu = static_cast<float>(total);
+        row_ctas = total > 0 ? min(max(static_cast<int>(ctas * wr / (wr + wu) + 0.5f), 1), ctas - 1) : ctas;
+      }
+      takes_rows = cta >= ctas - row_ctas;
+      if (takes_rows) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) sh[g] = pd_share(row_total, 2 * row_ctas, 2 * (cta - (ctas - row_ctas)) + g);
+        x0 = sh[0].x0;
+        x1 = max(sh[0].x1, sh[1].x1);
+        return;
+      }
       // a share is at least a pair step long, so each CTA between the first and the last one of a
       // unit has a key tile of it
-      G = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), total / (128 * kPfPair))));
+      G = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(ctas - row_ctas), total / (128 * kPfPair))));
       quot = div64(total, G);
       rem = static_cast<int>(total - quot * G);
       if (cta < G) {
@@ -247,41 +286,69 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         x1 = share_begin(cta + 1);
       }
     };
-    auto find = [&](int b, int64_t t, int64_t end) {  // sequence b's weights end at `end`
-      if (t > 0 && (end - t) * per_seq <= x0 && x0 < end * per_seq) {
-        s_first = b;
-        s_prefix = end - t;
+    auto find = [&](int b, const int64_t (&t)[2], const int64_t (&end)[2]) {  // sequence b's weights end at `end`
+      if (takes_rows) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (t[1] > 0 && (end[1] - t[1]) * p.Hkv <= sh[g].x0 && sh[g].x0 < end[1] * p.Hkv) {
+            s_first[g] = b;
+            s_prefix[g] = end[1] - t[1];
+          }
+      } else if (t[0] > 0 && (end[0] - t[0]) * per_seq <= x0 && x0 < end[0] * per_seq) {
+        s_first[0] = b;
+        s_prefix[0] = end[0] - t[0];
       }
     };
+    int64_t t[2], incl[2], all[2];
     if (p.B <= kPrefillThreads) {
-      const int64_t t = cost_of(threadIdx.x);
-      int64_t incl;
-      block_scan(t, incl, total);
-      total *= per_seq;
-      share();
+      costs_of(threadIdx.x, t);
+      block_scan(t, incl, all);
+      share(all);
       find(threadIdx.x, t, incl);
     } else {
-      int64_t mine = 0, incl, all;
-      for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) mine += cost_of(b);
-      block_scan(mine, incl, total);
-      total *= per_seq;
-      share();
-      int64_t base = 0;
-      for (int b0 = 0; b0 < p.B && x0 < x1 && base * per_seq <= x0; b0 += kPrefillThreads) {  // block-uniform
+      int64_t mine[2] = {0, 0}, base[2] = {0, 0};
+      for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) {
+        costs_of(b, t);
+        mine[0] += t[0];
+        mine[1] += t[1];
+      }
+      block_scan(mine, incl, all);
+      share(all);
+      for (int b0 = 0; b0 < p.B && x0 < x1; b0 += kPrefillThreads) {  // block-uniform
         const int b = b0 + static_cast<int>(threadIdx.x);
-        const int64_t t = cost_of(b);
+        costs_of(b, t);
         __syncthreads();  // s_sum's previous contents are read
         block_scan(t, incl, all);
-        find(b, t, base + incl);
-        base += all;
+        const int64_t end[2] = {base[0] + incl[0], base[1] + incl[1]};
+        find(b, t, end);
+        base[0] += all[0];
+        base[1] += all[1];
       }
     }
+    if (takes_rows && threadIdx.x == 0) {
+      // the space becomes that of two decode CTAs
+      for (int i = 0; i < Cfg::kNumBars; ++i) mbar_inval(bar0 + 8u * i);
+      for (int g = 0; g < 2; ++g) PdSmem<D>(smem + g * Cfg::kRowsBytes).init();
+    }
     __syncthreads();
+  }
+  // joins that nobody else writes: the units' of a CTA with short sequences, and the reverse
+  if (threadIdx.x < 2) {
+    if (takes_rows) a.joins[2 * cta + threadIdx.x] = make_int4(0, 0, 0, -1);
+    else if (rows.joins != nullptr) rows.joins[2 * (row_ctas + cta) + threadIdx.x] = make_int4(-1, 0, 0, 0);
   }
 
   if (warp >= 8) {
     regs_decrease<kCtrlRegs>();
-    if (warp == kLoadWarp) {
+    if (takes_rows) {
+      if (warp < 10) {
+        const int g = warp - 8;
+        PdShare my = g == 0 ? sh[0] : sh[1];
+        my.first = static_cast<int>(s_first[g]);
+        my.prefix = s_prefix[g];
+        pd_producer<D>(rows, PdSmem<D>(smem + g * Cfg::kRowsBytes), my, 2 * (cta - (ctas - row_ctas)) + g, lane);
+      }
+    } else if (warp == kLoadWarp) {
       // ------------------------------------------- producer and scheduler
       const int pb_shift = min(p.page_shift, 7);
       const int pb = 1 << pb_shift;         // rows per copy
@@ -296,7 +363,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       uint32_t tail_uses = 0;    // per slot: parity of the tiles handed to warp 11
       uint32_t slot_tail = 0;    // per slot: its last tile was one of them
       bool ok = true;
-      int4 join0 = make_int4(0, 0, 0, -1), join1 = make_int4(0, 0, 0, 0);
+      int4 join0 = make_int4(0, 0, 0, -1), join1 = make_int4(0, 0, 0, 0);  // the unit that a later share ends
+      int64_t join_last = 0;                                               // its last key tile's place
       auto page_of = [&](int b, int j, int L) -> int {  // the page of this lane's copy of key tile j
         const int key = j * 128 + box * pb;
         if (!copier || key >= L) return a.oob_page;
@@ -308,18 +376,18 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         return page;
       };
       if (x0 < x1) {
-        int b = static_cast<int>(s_first);
-        PfSeq s = pf_seq(a, b, false);
-        const int64_t in_seq = x0 - s_prefix * per_seq;
+        int b = static_cast<int>(s_first[0]);
+        PfSeq s = pf_seq(a, b);
+        const int64_t in_seq = x0 - s_prefix[0] * per_seq;
         int hr = static_cast<int>(div64(in_seq, s.cost));   // KV head * chunks + head tile
         const int64_t in_head = in_seq - hr * s.cost;
         int v = 0;
         for (int hi = s.units; hi - v > 1;) {  // last unit that begins at or before the share
           const int mid = (v + hi) >> 1;
-          if (pf_prefix(p.causal, mid, tu, s.L, s.coff) <= in_head) v = mid;
+          if (pf_prefix(a, mid, s.L, s.coff) <= in_head) v = mid;
           else hi = mid;
         }
-        int64_t xs = x0 - in_head + pf_prefix(p.causal, v, tu, s.L, s.coff);  // where the unit begins
+        int64_t xs = x0 - in_head + pf_prefix(a, v, s.L, s.coff);  // where the unit begins
         while (ok && xs < x1) {
           // unit (b, hr, v): tokens v tu .. of the sequence
           const int cnt0 = min(s.n - v * tu, a.tpt);
@@ -327,22 +395,27 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           const bool thin = cnt1 == 0;
           const int w = 128 * (thin ? kPfThin : kPfPair);  // weight of a key tile
           const int64_t t0 = static_cast<int64_t>(v) * tu;
-          const int keys = pf_visible(p.causal, t0 + cnt0 + cnt1, s.L, s.coff);
+          const int keys = paged_visible(p.causal, t0 + cnt0 + cnt1, s.L, s.coff);
           const int n_u = (keys + 127) / 128;                                          // its key tiles
-          const int n_0 = (pf_visible(p.causal, t0 + cnt0, s.L, s.coff) + 127) / 128;  // tile 0's
+          const int n_0 = (paged_visible(p.causal, t0 + cnt0, s.L, s.coff) + 127) / 128;  // tile 0's
           // key tile k stands at xs + kPfUnitCost + w k
           const bool split = n_u > (thin ? kPfWholeThin : kPfWholePair);
           auto tile_at = [&](int64_t x) -> int {
             const int64_t off = x - xs - kPfUnitCost;
             if (off <= 0) return 0;
-            return split ? static_cast<int>(min(static_cast<int64_t>(n_u), div64(off + w - 1, w))) : n_u;
+            if (!split) return n_u;
+            // (a division by a constant either way)
+            const uint64_t k = thin ? (static_cast<uint64_t>(off) + 128 * kPfThin - 1) / (128 * kPfThin)
+                                    : (static_cast<uint64_t>(off) + 128 * kPfPair - 1) / (128 * kPfPair);
+            return static_cast<int>(min(static_cast<uint64_t>(n_u), k));
           };
           const int j0 = tile_at(x0), j1 = tile_at(x1);
           const int64_t xe = xs + kPfUnitCost + static_cast<int64_t>(w / 128) * keys;
           if (j1 > j0 || (n_u == 0 && xs >= x0)) {
             const int steps = j1 - j0;
             const bool whole = steps == n_u;
-            const int hk = hr / a.chunks, chunk = hr - hk * a.chunks;
+            const int hk = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_chunks));
+            const int chunk = hr - hk * a.chunks;
             const int g0 = chunk * a.hc;
             const int heads = min(a.hc, p.group - g0);
             const int tok0 = s.start + static_cast<int>(t0);
@@ -355,12 +428,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               n1 = steps;
             }
             if (j0 == 0 && !whole) {
-              const int64_t last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * w;
-              // the CTA whose share holds the unit's last key tile
-              int c = static_cast<int>(div64(last, quot + 1));  // at most the right one
-              while (c + 1 < G && share_begin(c + 1) <= last) ++c;
-              join0 = make_int4(tok0, hk * p.group + g0, heads, c);
+              join0 = make_int4(tok0, hk * p.group + g0, heads, 0);
               join1 = make_int4(cnt0, cnt1, 0, 0);
+              join_last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * w;
             }
             // announce
             const int k = ui % kPfRing;
@@ -444,17 +514,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
             if (++hr == per_seq) {
               hr = 0;
               if (xs >= x1) break;
-              // the next sequence with tokens
+              // the next sequence with units
               unsigned some = 0u;
               for (++b; b < p.B && some == 0u; b += 32) {
-                some = __ballot_sync(0xffffffffu, b + lane < p.B && pf_seq(a, b + lane, false).n > 0);
+                some = __ballot_sync(0xffffffffu, b + lane < p.B && pf_seq(a, b + lane).units > 0);
                 if (some != 0u) b += __ffs(some) - 1 - 32;
               }
               if (some == 0u) break;
-              s = pf_seq(a, b, false);
+              s = pf_seq(a, b);
             }
           }
         }
+      }
+      if (join0.w >= 0) {  // the CTA whose share holds that place
+        int c = static_cast<int>(div64(join_last, quot + 1));  // at most the right one
+        while (c + 1 < G && share_begin(c + 1) <= join_last) ++c;
+        join0.w = c;
       }
       if (lane == 0) {
         a.joins[2 * cta] = join0;
@@ -600,6 +675,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       }
       __syncwarp();
     }
+  } else if (takes_rows) {
+    regs_increase<kSoftmaxRegs>();
+    pd_consumer<D>(rows, PdSmem<D>(smem + (warp >> 2) * Cfg::kRowsBytes), warp & 3, lane, 1 + (warp >> 2));
   } else {
     // Warpgroups 0 and 1: softmax and epilogue of tile 0 and 1.
     regs_increase<kSoftmaxRegs>();
@@ -867,37 +945,35 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   }
 }
 
-// Join the partials of the units that cross shares: blocks (c, tile, 16 columns) take the unit that
-// begins in CTA c's share, one thread per row, pieces in share order.
+// Join the partials of a unit that crosses shares: a block of 512 threads takes 64 columns of tile t
+// of the unit that begins in CTA c's share; one thread per row and 16 columns, pieces in share order.
 constexpr int kPfJoinCols = 16;
 
 template <int D>
-__global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a) {
+__device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta, int t, int col) {
   constexpr float kLog2e = 1.4426950408889634f;
   const PagedParams& p = a.p;
-  grid_dependency_trigger();
-  grid_dependency_wait();
-  const int cta = static_cast<int>(blockIdx.x), t = static_cast<int>(blockIdx.y);
-  const int col = static_cast<int>(blockIdx.z) * kPfJoinCols;
+  col += (static_cast<int>(threadIdx.x) >> 7) * kPfJoinCols;
   const int4 j0 = a.joins[2 * cta], j1 = a.joins[2 * cta + 1];
   if (j0.w < 0) return;
-  const int r = threadIdx.x;
+  const int r = threadIdx.x & 127;
   const int tok = static_cast<int>(fastdiv(static_cast<uint32_t>(r), a.div_hc));
   const int head = r - tok * a.hc;
   if (tok >= (t ? j1.y : j1.x) || head >= j0.z) return;
   const int pieces = j0.w - cta + 1;
   auto slot = [&](int s) { return (static_cast<int64_t>(2 * (cta + s) + (s == 0 ? 1 : 0)) * 2 + t) * 128; };
-  // one pass with a running maximum, two pieces' loads at a time
+  // one pass with a running maximum, the loads of kAhead pieces at a time
+  constexpr int kAhead = 4;
   float M = -INFINITY, W = 0.f;
   float acc[kPfJoinCols];
 #pragma unroll
   for (int i = 0; i < kPfJoinCols; ++i) acc[i] = 0.f;
 #pragma unroll 1
-  for (int s0 = 0; s0 < pieces; s0 += 2) {
-    float2 ml[2];
-    float x[2][kPfJoinCols];
+  for (int s0 = 0; s0 < pieces; s0 += kAhead) {
+    float2 ml[kAhead];
+    float x[kAhead][kPfJoinCols];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       ml[u] = make_float2(-INFINITY, 0.f);
       if (s0 + u < pieces) {
         ml[u] = a.part_ml[slot(s0 + u) + r];
@@ -907,7 +983,7 @@ __global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_consta
       }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       if (!(ml[u].y > 0.f)) continue;
       const float m_new = fmaxf(M, ml[u].x);
       const float down = M == -INFINITY ? 0.f : ex2_approx((M - m_new) * kLog2e);
@@ -929,6 +1005,20 @@ __global__ void __launch_bounds__(128) paged_fwd_join_kernel(const __grid_consta
   if (col == 0 && p.lse != nullptr)
     p.lse[static_cast<int64_t>(j0.y + head) * p.T + token] =
         W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
+}
+
+// Both kernels' joins in one launch: `units` CTAs of the tcgen05 kernel (2 tiles, d/64 column blocks
+// each), then `rows` CTAs of the decode kernel.
+template <int D>
+__global__ void __launch_bounds__(kPdRows * 32) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a,
+                                                                      const __grid_constant__ PagedDecodeParams d,
+                                                                      int units, int rows) {
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  constexpr int kPer = 2 * (D / 64);
+  const int x = static_cast<int>(blockIdx.x);
+  if (x < units * kPer) paged_fwd_join<D>(a, x / kPer, x & 1, (x % kPer >> 1) * 64);
+  else paged_decode_join<D>(d, x - units * kPer, rows);
 }
 
 }  // namespace sdpa

@@ -76,6 +76,8 @@ attn_status_t paged_params(PagedParams* p, const void* q, const attn_paged_cache
   p->num_pages = cache->num_pages;
   p->max_pages = cache->max_pages;
   p->page_shift = log2_of(cache->page_size);
+  p->div_group = make_fastdiv(static_cast<uint32_t>(p->group));
+  p->row_tokens = kRowUnit / p->group;
   p->causal = causal;
   p->scale = effective_scale(scale, d);
   p->scale_log2 = p->scale * 1.4426950408889634f;
@@ -99,6 +101,22 @@ bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch as a programmatic dependent of what precedes it on the stream.
+struct PdlLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  PdlLaunch(unsigned grid, int threads, int smem, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
 // The decode's workspace: two partial row sets and one join per CTA of the grid.
 size_t paged_decode_ws_bytes(int sms, int d) {
   return static_cast<size_t>(kPdCtasPerSm * sms) * (2 * kPdRows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
@@ -113,30 +131,35 @@ attn_status_t launch_paged_decode(const PagedDecodeParams& a, int sms, int dev, 
     std::lock_guard<std::mutex> lock(mu);
     if (!set_smem(paged_decode_kernel<D>, PagedDecodeCfg<D>::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(kPdCtasPerSm * sms));
-  cfg.blockDim = dim3(kPdThreads);
-  cfg.dynamicSmemBytes = PagedDecodeCfg<D>::kSmemBytes;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D>, a) != cudaSuccess) return ATTN_ERR_CUDA;
-  cfg.blockDim = dim3(kPdRows * 32);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  PdlLaunch l(static_cast<unsigned>(kPdCtasPerSm * sms), kPdThreads, PagedDecodeCfg<D>::kSmemBytes, st);
+  if (cudaLaunchKernelEx(&l.cfg, paged_decode_kernel<D>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+  PdlLaunch j(static_cast<unsigned>(kPdCtasPerSm * sms), kPdRows * 32, 0, st);
+  return cudaLaunchKernelEx(&j.cfg, paged_decode_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// The forward's workspace: two partial row sets of two tiles and one join per CTA of the grid.
-size_t paged_fwd_ws_bytes(int sms, int d) {
+// What the decode kernel needs besides the parameters: tensor maps over the pages (`q` where there are
+// none), and its part of the workspace.
+bool paged_rows_params(PagedDecodeParams* a, int d, int sms, void* workspace) {
+  const bool pages = a->p.num_pages > 0;
+  a->oob_page = std::max(a->p.num_pages, 1);
+  const int box = std::min(1 << a->p.page_shift, kPdKeys);
+  a->part_o = static_cast<float*>(workspace);
+  a->part_ml = reinterpret_cast<float2*>(a->part_o + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows * d);
+  a->joins = reinterpret_cast<int4*>(a->part_ml + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows);
+  return make_page_map(&a->tm_k, pages ? a->p.k : a->p.q, a->p, d, box, d / 64) &&
+         make_page_map(&a->tm_v, pages ? a->p.v : a->p.q, a->p, d, box, d / 64);
+}
+
+// The forward's own part of its workspace: two partial row sets of two tiles and one join per CTA; the
+// decode's part follows.
+size_t paged_units_ws_bytes(int sms, int d) {
   return static_cast<size_t>(sms) * (2 * 2 * 128 * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
                                      2 * sizeof(int4));
 }
 
 template <int D, int NS>
-attn_status_t launch_paged_fwd(const PagedFwdParams& a, int sms, int dev, cudaStream_t st) {
+attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams& r, int sms, int dev,
+                               cudaStream_t st) {
   static bool smem_done[kMaxDevices] = {};
   static std::mutex mu;
   using Cfg = PagedFwdCfg<D, NS>;
@@ -150,21 +173,12 @@ attn_status_t launch_paged_fwd(const PagedFwdParams& a, int sms, int dev, cudaSt
     }
     if (!set_smem(paged_fwd_kernel<D, NS>, Cfg::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms));
-  cfg.blockDim = dim3(kPrefillThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D, NS>, a) != cudaSuccess) return ATTN_ERR_CUDA;
-  cfg.gridDim = dim3(static_cast<unsigned>(sms), 2, D / kPfJoinCols);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_fwd_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  PdlLaunch l(static_cast<unsigned>(sms), kPrefillThreads, Cfg::kSmemBytes, st);
+  if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
+  const int rows = r.joins != nullptr ? kPdCtasPerSm * sms : 0;
+  PdlLaunch j(static_cast<unsigned>(sms * 2 * (D / 64) + rows), kPdRows * 32, 0, st);
+  return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r, sms, rows) == cudaSuccess ? ATTN_OK
+                                                                                              : ATTN_ERR_CUDA;
 }
 
 // 4-D map (d, head in group, KV head, token) over q [T, Hq, d]; box {64, hc, 1, tpt}, 128-byte swizzle.
@@ -294,7 +308,8 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
 
 size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {
   if (T < 0 || T > kMaxSeq || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return paged_fwd_ws_bytes(sm_count_or_default(), d);
+  const int sms = sm_count_or_default();
+  return paged_units_ws_bytes(sms, d) + (Hq / Hkv <= kRowUnit ? paged_decode_ws_bytes(sms, d) : 0);
 }
 
 attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, const int* cu_q, const int* seqlens_k,
@@ -317,6 +332,8 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, con
   a.hc = (group + a.chunks - 1) / a.chunks;
   a.tpt = 128 / a.hc;
   a.div_hc = make_fastdiv(static_cast<uint32_t>(a.hc));
+  a.div_tu = make_fastdiv(static_cast<uint32_t>(2 * a.tpt));
+  a.div_chunks = make_fastdiv(static_cast<uint32_t>(a.chunks));
   const bool pages = a.p.num_pages > 0;
   a.oob_page = std::max(a.p.num_pages, 1);
   const int box = std::min(1 << a.p.page_shift, 128);
@@ -327,9 +344,20 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, con
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(sms) * 4 * 128 * d);
   a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(sms) * 4 * 128);
+  PagedDecodeParams r;
+  std::memset(&r, 0, sizeof(r));
+  if (group <= kRowUnit) {  // else no sequence is short enough
+    r.p = a.p;
+    r.row_groups = 1;
+    r.div_rg = make_fastdiv(1);
+    r.lse_tok = 1;
+    r.lse_head = T;
+    if (!paged_rows_params(&r, d, sms, static_cast<uint8_t*>(workspace) + paged_units_ws_bytes(sms, d)))
+      return ATTN_ERR_CUDA;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged_fwd<128, kStagesD128>(a, sms, dev, st)
-                  : launch_paged_fwd<64, kStagesD64>(a, sms, dev, st);
+  return d == 128 ? launch_paged_fwd<128, kStagesD128>(a, r, sms, dev, st)
+                  : launch_paged_fwd<64, kStagesD64>(a, r, sms, dev, st);
 }
 
 size_t attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
@@ -357,16 +385,11 @@ attn_status_t attn_decode_splitkv_paged(const void* q, const attn_paged_cache_t*
   const int64_t rows = static_cast<int64_t>(a.p.group) * Sq;
   if (rows > INT_MAX / 2) return ATTN_ERR_SHAPE;
   a.row_groups = static_cast<int>((rows + kPdRows - 1) / kPdRows);
+  a.div_rg = make_fastdiv(static_cast<uint32_t>(a.row_groups));
   if (static_cast<int64_t>(Hkv) * a.row_groups > INT_MAX / 2) return ATTN_ERR_SHAPE;
-  const bool pages = a.p.num_pages > 0;
-  a.oob_page = std::max(a.p.num_pages, 1);
-  const int box = std::min(1 << a.p.page_shift, kPdKeys);
-  if (!make_page_map(&a.tm_k, pages ? cache->k_pages : q, a.p, d, box, d / 64) ||
-      !make_page_map(&a.tm_v, pages ? cache->v_pages : q, a.p, d, box, d / 64))
-    return ATTN_ERR_CUDA;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows * d);
-  a.joins = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(2 * kPdCtasPerSm * sms) * kPdRows);
+  a.lse_tok = Hq;
+  a.lse_head = Sq;
+  if (!paged_rows_params(&a, d, sms, workspace)) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d == 128 ? launch_paged_decode<128>(a, sms, dev, st) : launch_paged_decode<64>(a, sms, dev, st);
 }
