@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdpa_b200.so")
@@ -37,6 +38,10 @@ class PagedCache(ctypes.Structure):
     _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("page_stride", ctypes.c_longlong), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+# The same as packed bytes, which cost less to make than a Structure.
+pack_paged_cache = struct.Struct("@PPPqiiii").pack
 
 
 _lock = threading.Lock()
@@ -81,7 +86,7 @@ def _declare(lib):
     lib.attn_bwd.restype = I
     lib.attn_bwd_workspace_size.argtypes = [I, I, I]
     lib.attn_bwd_workspace_size.restype = SZ
-    PC = ctypes.POINTER(PagedCache)
+    PC = ctypes.c_void_p  # a PagedCache (byref) or its packed bytes
     lib.attn_page_plan.argtypes = [P] * 10 + [I] * 5 + [P]
     lib.attn_page_plan.restype = I
     lib.attn_rope_append_paged.argtypes = [P, P, P, I, P, P, P, PC, I, I, I, I, P]

@@ -14,8 +14,9 @@
 
 namespace sdpa {
 
-// A sequence of the forward's batch that brings no more query rows of a KV head
-// than this (a single token, mostly) is the decode's work.
+// The forward takes a sequence's tokens in units of two 128-row tiles.  What the
+// full units leave is the decode's work where it is no more query rows of a KV
+// head than this: a single token's, mostly.
 constexpr int kRowUnit = 16;
 
 struct PagedParams {
@@ -33,7 +34,9 @@ struct PagedParams {
   int causal;          // 0 none, 1 top-left, 2 bottom-right
   float scale, scale_log2;
   FastDiv div_group;
-  int row_tokens;      // tokens of a sequence that is the decode's work: kRowUnit / group
+  int row_tokens;      // ragged batch: tokens that kRowUnit rows hold, kRowUnit / group
+  int unit_tokens;     // ragged batch: tokens of a full unit
+  FastDiv div_tu;      // by unit_tokens
 };
 
 // A number of keys, clamped to what a row of the table can hold (2^30 at most).

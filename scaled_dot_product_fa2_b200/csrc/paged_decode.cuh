@@ -72,8 +72,8 @@ struct PagedDecodeCfg {
 // Tiles of an item over `len` keys; an empty one takes one as well (its rows are written).
 __device__ __forceinline__ int pd_tiles(int len) { return max(1, (len + kPdKeys - 1) / kPdKeys); }
 
-// The tokens of sequence b: all of the decode's Sq; those of a ragged sequence
-// where they are few (kRowUnit).
+// The tokens of sequence b: all of the decode's Sq; what the full units leave of
+// a ragged sequence, where it is little (kRowUnit).
 struct PdSeq {
   int tok0, cnt;  // first token's row of q, tokens (0: no item)
   int L;          // keys that any of them sees
@@ -83,10 +83,12 @@ struct PdSeq {
 
 __device__ __forceinline__ PdSeq pd_of(const PagedParams& p, const PagedSeq& q) {
   PdSeq s;
-  s.tok0 = q.start;
-  s.cnt = q.n <= p.row_tokens ? q.n : 0;
-  s.lim = p.causal == 2 ? q.L - q.n : 0;
-  s.L = paged_visible(p.causal, q.n, q.L, s.lim);
+  const int left = q.n - static_cast<int>(fastdiv(static_cast<uint32_t>(q.n), p.div_tu)) * p.unit_tokens;
+  s.cnt = left <= p.row_tokens ? left : 0;
+  s.tok0 = q.start + q.n - s.cnt;
+  const int coff = p.causal == 2 ? q.L - q.n : 0;
+  s.L = paged_visible(p.causal, q.n, q.L, coff);
+  s.lim = coff + q.n - s.cnt;
   s.T = s.cnt > 0 ? pd_tiles(s.L) : 0;
   return s;
 }

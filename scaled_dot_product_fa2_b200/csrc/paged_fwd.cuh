@@ -22,9 +22,9 @@
 //     place from the lengths on the device.  A unit that crosses shares leaves
 //     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
 //     programmatic dependent, joins in share order.
-//   * Sequences of no more than kRowUnit rows (a single token of up to 16 heads)
-//     are the decode's work: a 128-row tile would load the same bytes at a lower
-//     rate.  They form a line of their own, and the grid's last CTAs, in the
+//   * What a sequence leaves behind its full units is the decode's work where it
+//     is no more than kRowUnit rows (a single token of up to 16 heads): a 128-row
+//     tile would load the same bytes at a lower rate.  They form a line of their own, and the grid's last CTAs, in the
 //     proportion of the two lines' times, each run as two of the decode kernel's
 //     CTAs (paged_decode.cuh): the bytes stream while the other SMs multiply.
 //   * K/V tiles of 128 keys arrive as one TMA copy per page (or 128 rows of it)
@@ -58,7 +58,7 @@ struct PagedFwdParams {
   int oob_page;       // a page index behind the map's last one (reads as zeros)
   int hc, chunks;     // heads per tile, tiles of heads per group
   int tpt;            // tokens per tile: 128 / hc
-  FastDiv div_hc, div_tu, div_chunks;  // by hc, 2 tpt, chunks
+  FastDiv div_hc, div_chunks;  // by hc, chunks
   float* part_o;      // [2 * CTAs][2 tiles][d][128 rows] locally normalised partial outputs
   float2* part_ml;    // [2 * CTAs][2 tiles][128] (max of scale * q.k, sum)
   int4* joins;        // [CTAs][2] {first token, first head, heads, last CTA (-1: no join)}, {tokens of tile 0, 1, -, -}
@@ -75,7 +75,7 @@ struct PagedFwdCfg {
   static constexpr int kRingOffset = (kNumBars * 8 + 15) / 16 * 16;   // pieces: kPfRing x 16 ints
   static constexpr int kMergeOffset = kRingOffset + kPfRing * 64;     // thin units: (max, sum) of tile 1's rows
   static constexpr int kEnd = (2 + NS) * kTileBytes + kMergeOffset + 128 * 8;
-  // a CTA that takes short sequences holds two of the decode's CTAs instead
+  // a CTA that takes such rows holds two of the decode's CTAs instead
   static constexpr int kRowsBytes = (PagedDecodeCfg<D>::kSumOffset + 1023) / 1024 * 1024;
   // above both: sums of 12 warps and two lines, prefix and first sequence of two shares, TMEM base, abort flag
   static constexpr int kSumOffset = kEnd > 2 * kRowsBytes ? kEnd : 2 * kRowsBytes;
@@ -87,7 +87,7 @@ struct PagedFwdCfg {
 struct PfSeq {
   int start, n;     // first token, tokens
   int L, coff;      // keys; token i sees key j iff j <= i + coff (causal)
-  int full, units;  // units whose two tiles are full, units (none in a short sequence)
+  int full, units;  // units whose two tiles are full, units (without one that is the decode's work)
   int64_t cost;     // weight of its units for one (KV head, head tile)
 };
 
@@ -97,7 +97,7 @@ __device__ __forceinline__ int64_t pf_prefix(const PagedFwdParams& a, int V, int
   const int64_t fixed = static_cast<int64_t>(V) * kPfUnitCost;
   if (!a.p.causal || V == 0) return fixed + kPfPair * static_cast<int64_t>(V) * L;
   const int tu = 2 * a.tpt;
-  auto div = [&](int x) { return static_cast<int>(fastdiv(static_cast<uint32_t>(x), a.div_tu)); };
+  auto div = [&](int x) { return static_cast<int>(fastdiv(static_cast<uint32_t>(x), a.p.div_tu)); };
   const int lo = min(V, div(max(-coff, 0)));                     // units that see nothing
   const int hi = min(V, max(lo, div(L - coff + tu - 1) - 1));    // first unit that sees every key
   const int64_t m = hi - lo;
@@ -112,9 +112,9 @@ __device__ __forceinline__ PfSeq pf_of(const PagedFwdParams& a, const PagedSeq& 
   s.n = q.n;
   s.L = q.L;
   s.coff = p.causal == 2 ? s.L - s.n : 0;
-  s.full = static_cast<int>(fastdiv(static_cast<uint32_t>(s.n), a.div_tu));
+  s.full = static_cast<int>(fastdiv(static_cast<uint32_t>(s.n), a.p.div_tu));
   const int rem = s.n - s.full * 2 * a.tpt;
-  const bool more = rem > 0 && s.n > p.row_tokens;
+  const bool more = rem > p.row_tokens;
   s.units = s.full + (more ? 1 : 0);
   s.cost = pf_prefix(a, s.full, s.L, s.coff);
   if (more)
@@ -501,8 +501,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
                 slot_tail = (slot_tail & ~(1u << slot)) | ((to_clean ? 1u : 0u) << slot);
                 if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
                 __syncwarp();
-                if (copier)
-                  tma_load_5d(sKV + slot * Cfg::kTileBytes + box_dst, kv ? &a.tm_v : &a.tm_k, 0, row, blk, hk, cur, bar);
+                if (copier) {
+                  const uint32_t dst = sKV + slot * Cfg::kTileBytes + box_dst;
+                  const CUtensorMap* const tm = kv ? &a.tm_v : &a.tm_k;
+                  // a lone unit's keys are read once (see pd_producer)
+                  if (s.units == 1) tma_load_5d_hint(dst, tm, 0, row, blk, hk, cur, bar, l2_evict_first());
+                  else tma_load_5d(dst, tm, 0, row, blk, hk, cur, bar);
+                }
               }
             }
             ++ui;

@@ -332,7 +332,8 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, con
   a.hc = (group + a.chunks - 1) / a.chunks;
   a.tpt = 128 / a.hc;
   a.div_hc = make_fastdiv(static_cast<uint32_t>(a.hc));
-  a.div_tu = make_fastdiv(static_cast<uint32_t>(2 * a.tpt));
+  a.p.unit_tokens = 2 * a.tpt;
+  a.p.div_tu = make_fastdiv(static_cast<uint32_t>(a.p.unit_tokens));
   a.div_chunks = make_fastdiv(static_cast<uint32_t>(a.chunks));
   const bool pages = a.p.num_pages > 0;
   a.oob_page = std::max(a.p.num_pages, 1);

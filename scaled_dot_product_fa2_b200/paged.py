@@ -7,21 +7,26 @@ by its index, and the device context is entered only where it changes something.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _lib
 from .ops import CAUSAL_BOTTOM_RIGHT, LAYOUT_BHSD, LAYOUT_BSHD, _stream_handle
 
 _BF16, _INT32, _FP32 = torch.bfloat16, torch.int32, torch.float32
-# the current stream of a device as an integer, without a Stream object where torch offers that
+_Tensor = torch.Tensor
+# the current device, and the current stream of one as an integer (without a Stream object), where torch
+# offers them directly
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream_handle
+
+
+def _is_tensor(t):
+    return type(t) is _Tensor or isinstance(t, _Tensor)  # isinstance alone asks torch's metaclass
 
 
 def _call(fn, name, index, *args):
     """One entry point on the current stream of device `index`."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -32,7 +37,7 @@ def _call(fn, name, index, *args):
 
 def _tensor(name, t, dtype, ndim):
     """The device index of a contiguous CUDA tensor of this type."""
-    if not isinstance(t, torch.Tensor):
+    if not _is_tensor(t):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -48,7 +53,7 @@ def _tensor(name, t, dtype, ndim):
 
 def _ints(name, t, n, index):
     """The address of a contiguous int32 tensor [n] on device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.dim() != 1:
+    if not _is_tensor(t) or t.dtype is not _INT32 or t.dim() != 1:
         raise TypeError(f"{name} must be an int32 tensor [{n}]")
     if t.numel() != n or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor on cuda:{index}, got {tuple(t.shape)}")
@@ -57,7 +62,7 @@ def _ints(name, t, n, index):
 
 def _table(t, B, index):
     """(address, entries per row) of a block table."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.dim() != 2:
+    if not _is_tensor(t) or t.dtype is not _INT32 or t.dim() != 2:
         raise TypeError("block_table must be an int32 tensor [B, max_pages]")
     rows, width = t.shape
     if rows != B or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
@@ -66,10 +71,10 @@ def _table(t, B, index):
 
 
 def _pages(k_pages, v_pages, layout, index, table=0, max_pages=0):
-    """(attn_paged_cache_t, Hkv, d) of two page pools [N, Hkv, P, d] ([N, P, Hkv, d] for
+    """(attn_paged_cache_t as bytes, Hkv, d) of two page pools [N, Hkv, P, d] ([N, P, Hkv, d] for
     LAYOUT_BSHD), dense inside a page and of one stride between pages."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+        if not _is_tensor(t) or t.dtype is not _BF16:
             raise TypeError(f"{name} must be a torch.bfloat16 tensor")
         if t.dim() != 4:
             raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
@@ -89,8 +94,8 @@ def _pages(k_pages, v_pages, layout, index, table=0, max_pages=0):
         P, Hkv = s1, s2
     else:
         raise ValueError(f"unknown layout {layout}")
-    return _lib.PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), table, sk[0] if N > 1 else 0, N, P, max_pages,
-                           layout), Hkv, d
+    return _lib.pack_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), table, sk[0] if N > 1 else 0, N, P,
+                                 max_pages, layout), Hkv, d
 
 
 def _outputs(q, lse_shape, out, lse, return_lse, index):
@@ -108,7 +113,7 @@ def _outputs(q, lse_shape, out, lse, return_lse, index):
 
 def _workspace(t, index):
     """(address, bytes) of a workspace."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if not _is_tensor(t) or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous buffer on q's device")
     return t.data_ptr(), t.numel() * t.element_size()
 
@@ -130,7 +135,7 @@ def attn_page_plan(past_lens, new_lens, block_table, free_pages, free_range, pag
     B = past_lens.shape[0]
     new = _ints("new_lens", new_lens, B, index)
     table, width = _table(block_table, B, index)
-    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+    if not _is_tensor(free_pages) or free_pages.dim() != 1:
         raise TypeError("free_pages must be an int32 tensor [num_free]")
     num_free = free_pages.shape[0]
     free = _ints("free_pages", free_pages, num_free, index)
@@ -174,7 +179,7 @@ def attn_rope_append_paged(packed_qkv, cos, sin, positions, slot_map, k_pages, v
     elif _tensor("q_out", q_out, _BF16, 3) != index or q_out.shape != (T, Hq, d):
         raise ValueError(f"q_out must be {(T, Hq, d)} on packed_qkv's device")
     _call(_lib.get().attn_rope_append_paged, "attn_rope_append_paged", index, packed_qkv.data_ptr(), cos.data_ptr(),
-          sin.data_ptr(), cos.shape[0], pos, slot, q_out.data_ptr(), ctypes.byref(cache), T, Hq, Hkv, d)
+          sin.data_ptr(), cos.shape[0], pos, slot, q_out.data_ptr(), cache, T, Hq, Hkv, d)
     return q_out
 
 
@@ -220,7 +225,7 @@ def attn_fwd_paged(q, k_pages, v_pages, cu_q, seqlens_k, block_table, causal: in
     """
     index = _tensor("q", q, _BF16, 3)
     T, Hq, d = q.shape
-    if not isinstance(seqlens_k, torch.Tensor) or seqlens_k.dim() != 1:
+    if not _is_tensor(seqlens_k) or seqlens_k.dim() != 1:
         raise TypeError("seqlens_k must be an int32 tensor [B]")
     B = seqlens_k.shape[0]
     lens, cu = _ints("seqlens_k", seqlens_k, B, index), _ints("cu_q", cu_q, B + 1, index)
@@ -231,7 +236,7 @@ def attn_fwd_paged(q, k_pages, v_pages, cu_q, seqlens_k, block_table, causal: in
     if workspace is None:
         workspace = fwd_paged_workspace(q, k_pages, layout)
     ws, ws_bytes = _workspace(workspace, index)
-    _call(_lib.get().attn_fwd_paged, "attn_fwd_paged", index, q.data_ptr(), ctypes.byref(cache), cu, lens,
+    _call(_lib.get().attn_fwd_paged, "attn_fwd_paged", index, q.data_ptr(), cache, cu, lens,
           out.data_ptr(), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, d, scale, causal, ws, ws_bytes)
     return out, lse
 
@@ -255,6 +260,6 @@ def attn_decode_splitkv_paged(q, k_pages, v_pages, seqlens_k, block_table, causa
         workspace = decode_paged_workspace(q, k_pages, layout)
     ws, ws_bytes = _workspace(workspace, index)
     _call(_lib.get().attn_decode_splitkv_paged, "attn_decode_splitkv_paged", index, q.data_ptr(),
-          ctypes.byref(cache), lens, out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, Sq, d,
+          cache, lens, out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, Sq, d,
           scale, causal, ws, ws_bytes)
     return out, lse

@@ -110,6 +110,11 @@ def test_fwd_rejects_bad_row_offsets_on_host(lib):
     assert fwd(lib, T=-1) == SHAPE
 
 
+def test_packed_cache_has_the_layout_of_the_struct():
+    c = _lib.PagedCache(1, 2, 3, 4, 5, 6, 7, 1)
+    assert _lib.pack_paged_cache(1, 2, 3, 4, 5, 6, 7, 1) == bytes(c)
+
+
 def test_null_cache_is_refused(lib):
     assert append(lib, c=ctypes.POINTER(_lib.PagedCache)()) == NULL
     assert fwd(lib, c=ctypes.POINTER(_lib.PagedCache)()) == NULL
