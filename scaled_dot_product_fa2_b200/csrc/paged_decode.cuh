@@ -613,7 +613,10 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) sm.init();
+  if (threadIdx.x == 0) {
+    sm.init();
+    s_first = s_prefix = 0;
+  }
   if (warp == kPdWarps && lane == 0) {
     tma_prefetch_desc(&a.tm_k);
     tma_prefetch_desc(&a.tm_v);

@@ -48,7 +48,7 @@ constexpr float kPfRowPlace = 150.f;      // a place on the short sequences' lin
 // Units of this many key tiles or fewer are not split: joining costs more.
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
-constexpr int kPfTailWarp = 11;
+constexpr int kPfQWarp = 11;     // loads Q; cleans V's last tile
 
 struct PagedFwdParams {
   PagedParams p;
@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
     mbar_init(drain, 2);
     for (int k = 0; k < kPfRing; ++k) {
       mbar_init(unit_full(k), 1);
-      mbar_init(unit_empty(k), 2 + 8 + 1);  // MMA threads, softmax warps, tail warp
+      mbar_init(unit_empty(k), 2 + 8 + 1);  // MMA threads, softmax warps, warp 11
     }
     mbar_init(merge_full, 4);
     mbar_init(merge_done, 4);
+    s_first[0] = s_first[1] = s_prefix[0] = s_prefix[1] = 0;
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -357,7 +358,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       const bool copier = blk < Cfg::kBlocks;
       const uint32_t box_dst = static_cast<uint32_t>(blk) * Cfg::kBlockBytes + static_cast<uint32_t>(box) * pb * 128u;
       const int tu = 2 * a.tpt;
-      const uint32_t q_bytes = static_cast<uint32_t>(a.hc) * a.tpt * D * 2;
       int it = 0;    // K/V tiles issued so far
       int ui = 0;    // pieces started so far
       uint32_t tail_uses = 0;    // per slot: parity of the tiles handed to warp 11
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               join1 = make_int4(cnt0, cnt1, 0, 0);
               join_last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * w;
             }
+            int page = page_of(b, j0, s.L);
             // announce
             const int k = ui % kPfRing;
             ok = __all_sync(0xffffffffu,
@@ -456,34 +457,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               mbar_arrive(unit_full(k));
             }
             __syncwarp();
-            // Q_0, Q_1: each once the previous piece's last S MMA on that buffer is done
-            auto load_q = [&]() -> bool {
-              for (int t = 0; t < 2; ++t) {
-                if (ui > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty(t), (ui - 1) & 1, abort_flag))) return false;
-                if (lane == 0) {
-                  if ((t ? n1 : n0) > 0) {
-                    mbar_arrive_expect_tx(q_full(t), q_bytes);
-                    for (int c = 0; c < Cfg::kBlocks; ++c)
-                      tma_load_4d(sQ + t * Cfg::kTileBytes + c * Cfg::kBlockBytes, &a.tm_q, c * 64, g0, hk,
-                                  tok0 + (thin ? 0 : t * a.tpt), q_full(t));
-                  } else {
-                    mbar_arrive(q_full(t));
-                  }
-                }
-                __syncwarp();
-              }
-              return true;
-            };
-            int page = page_of(b, j0, s.L);
-            const bool q_first = steps <= 1 || ui == 0;  // nothing to wait for
-            if (q_first) ok = load_q();
 #pragma unroll 1
             for (int x = 0; ok && x < steps; ++x) {
               const int j = j0 + x;
-              if (x == 1 && !q_first && !load_q()) {  // after K_0, V_0
-                ok = false;
-                break;
-              }
               const int cur = page;
               if (x + 1 < steps) page = page_of(b, j + 1, s.L);
               const int row = (j * 128 + box * pb) & ((1 << p.page_shift) - 1);
@@ -550,10 +526,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       }
       // Copies still in flight must land before the CTA may exit.
       if (lane == 0) {
-        if (ui > 0) {
-          mbar_wait_drain(q_full(0), (ui - 1) & 1);
-          mbar_wait_drain(q_full(1), (ui - 1) & 1);
-        }
         for (int i = max(0, it - NS); i < it; ++i) {
           const int slot = i % NS;
           if ((slot_tail >> slot) & 1u) mbar_wait_drain(tail(slot), ((tail_uses >> slot) & 1u) ^ 1u);
@@ -561,8 +533,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         }
       }
       __syncwarp();
-    } else if (warp == kPfTailWarp) {
-      // ------------------------------------------------ cleaner of V's last tile
+    } else if (warp == kPfQWarp) {
+      // ----------------------------- Q loader, and cleaner of V's last tile
+      // Q_0, Q_1: each once the previous piece's last S MMA on that buffer is
+      // done (a tile without key tiles only completes the phase).
+      const uint32_t q_bytes = static_cast<uint32_t>(a.hc) * a.tpt * D * 2;
+      int loaded[2] = {0, 0};  // pieces whose Q_t was loaded
       int it_base = 0;
       uint32_t tail_uses = 0;
       bool ok = true;
@@ -571,7 +547,29 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         volatile int* const e = next_piece(r, ok);
         if (e == nullptr) break;
         const int L = e[kKeys], steps = e[kSteps], j_last = e[kJ0] + steps - 1;
+        const int hk = e[kHead], g0 = e[kG0] - hk * p.group, tok0 = e[kTok0];
+        const int n[2] = {e[kN0], e[kN1]};
+        const int tok1 = tok0 + (e[kThin] ? 0 : a.tpt);
         release(r);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && (loaded[t] == 0 ||
+                      __all_sync(0xffffffffu, mbar_wait(q_empty(t), (loaded[t] - 1) & 1, abort_flag)));
+          if (!ok) break;
+          if (lane == 0) {
+            if (n[t] > 0) {
+              mbar_arrive_expect_tx(q_full(t), q_bytes);
+              for (int c = 0; c < Cfg::kBlocks; ++c)
+                tma_load_4d(sQ + t * Cfg::kTileBytes + c * Cfg::kBlockBytes, &a.tm_q, c * 64, g0, hk, t ? tok1 : tok0,
+                            q_full(t));
+            } else {
+              mbar_arrive(q_full(t));
+            }
+          }
+          ++loaded[t];
+          __syncwarp();
+        }
+        if (!ok) break;
         if (steps > 0 && (j_last + 1) * 128 > L) {
           const int itv = it_base + 2 * steps - 1;
           const int slot = itv % NS;
@@ -589,6 +587,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         }
         it_base += 2 * steps;
       }
+      // the last copies must land before the CTA may exit
+      if (lane == 0)
+        for (int t = 0; t < 2; ++t)
+          if (loaded[t] > 0) mbar_wait_drain(q_full(t), (loaded[t] - 1) & 1);
       __syncwarp();
     } else {
       // ---------------------------------------------- MMA issuer of tile t
