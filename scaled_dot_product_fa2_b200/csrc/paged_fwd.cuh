@@ -41,9 +41,9 @@ namespace sdpa {
 
 // Weights on the line.  A step of 128 keys takes 2.1 us in a pair (both softmax
 // chains) and 1.7 us per tile in a thin unit (bound by the bytes that its
-// ring keeps in flight); a unit costs 2.8 us besides (first S, last P.V, stores).
+// ring keeps in flight); a unit costs 3.2 us besides (first S, last P.V, stores).
 constexpr int kPfPair = 8, kPfThin = 6;   // per key
-constexpr int kPfUnitCost = 1400;
+constexpr int kPfUnitCost = 1600;
 constexpr float kPfRowPlace = 150.f;      // a place on the short sequences' line: 0.4 us of an SM
 // Units of this many key tiles or fewer are not split: joining costs more.
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
