@@ -39,6 +39,7 @@ constexpr int kPdCtasPerSm = 2;
 constexpr int kPdThreads = kPdWarps * 32 + 32;
 constexpr int kPdSegRing = 4;               // pieces announced ahead by the producer
 constexpr int kPdItemCost = 2;              // an item's fixed cost (query loads, merge, writes) in tiles
+constexpr int kPdWhole = 4;                 // items of this many tiles or fewer are not split: joining costs more
 
 struct PagedDecodeParams {
   PagedParams p;
@@ -245,8 +246,11 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
     };
     int page = page_of(b, tile, s.L);
     while (ok && xs + kPdItemCost < sh.x1) {
-      // a piece: tiles tile .. of item (b, hr), to its end or the share's
-      const int n = static_cast<int>(min(static_cast<int64_t>(s.T), sh.x1 - xs - kPdItemCost)) - tile;
+      // a piece: tiles tile .. of item (b, hr), to its end or the share's; an item that is not split
+      // belongs to the share that holds its first tile's place
+      const bool small = s.T <= kPdWhole;
+      const int n = small ? (tile == 0 ? s.T : 0)
+                          : static_cast<int>(min(static_cast<int64_t>(s.T), sh.x1 - xs - kPdItemCost)) - tile;
       const bool whole = tile == 0 && n == s.T;
       const int head = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_rg));
       {
@@ -262,12 +266,12 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
       }
       if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != s.L)
         atomicOr(&g_error_word, kErrSeqlen);
-      if (tile == 0 && n < s.T) {
+      if (tile == 0 && n < s.T) {  // (never a small one)
         join = make_int4(s.tok0, hr, 0, s.cnt);
         join_end = xs + kPdItemCost + s.T;
       }
       const int nk = s.L > 0 ? n : 0;
-      announce(s, hr, tile, nk, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
+      if (n > 0) announce(s, hr, tile, nk, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
       const int64_t xe = xs + kPdItemCost + s.T;
       const bool more = xe + kPdItemCost < sh.x1;  // the next item has tiles in this share
       int nb2 = b, nhr = hr + 1;

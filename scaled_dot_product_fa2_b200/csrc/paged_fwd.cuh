@@ -1014,18 +1014,30 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
         W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
 }
 
-// Both kernels' joins in one launch: `units` CTAs of the tcgen05 kernel (2 tiles, d/64 column blocks
-// each), then `rows` CTAs of the decode kernel.
+// Both lines' joins in one launch of one block per CTA of the forward, all of which fit on the device
+// at once: they are there when the grid before ends.  Block b looks at the units of shares b, b - 1, ..
+// (part k of share b - k: its tiles and 64-column blocks go to neighbouring blocks) and at the rows of
+// shares 2b and 2b + 1; what has nothing to join costs one look.
 template <int D>
 __global__ void __launch_bounds__(kPdRows * 32) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a,
-                                                                      const __grid_constant__ PagedDecodeParams d,
-                                                                      int units, int rows) {
+                                                                      const __grid_constant__ PagedDecodeParams d) {
   grid_dependency_trigger();
+  constexpr int kParts = 2 * (D / 64);
+  const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
+  auto share = [&](int k) { return b >= k ? b - k : b - k + n; };
+  const bool rows = d.joins != nullptr;
   grid_dependency_wait();
-  constexpr int kPer = 2 * (D / 64);
-  const int x = static_cast<int>(blockIdx.x);
-  if (x < units * kPer) paged_fwd_join<D>(a, x / kPer, x & 1, (x % kPer >> 1) * 64);
-  else paged_decode_join<D>(d, x - units * kPer, rows);
+  unsigned units = 0, items = 0;  // what there is to join
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) units |= (a.joins[2 * share(k)].w >= 0 ? 1u : 0u) << k;
+#pragma unroll
+  for (int k = 0; k < kPdCtasPerSm; ++k) items |= (rows && d.joins[kPdCtasPerSm * b + k].x >= 0 ? 1u : 0u) << k;
+#pragma unroll 1
+  for (int k = 0; k < kParts; ++k)
+    if ((units >> k) & 1u) paged_fwd_join<D>(a, share(k), k & 1, (k >> 1) * 64);
+#pragma unroll 1
+  for (int k = 0; k < kPdCtasPerSm; ++k)
+    if ((items >> k) & 1u) paged_decode_join<D>(d, kPdCtasPerSm * b + k, kPdCtasPerSm * n);
 }
 
 }  // namespace sdpa

@@ -117,6 +117,12 @@ struct PdlLaunch {
   }
 };
 
+// Whether an item or unit can be split at all: the table must hold more keys than those that stay whole.
+static_assert(kPdWhole * kPdKeys == kPfWholePair * 128 && kPfWholeThin >= kPfWholePair, "one limit for all of them");
+bool paged_can_split(const PagedParams& p) {
+  return (static_cast<int64_t>(p.max_pages) << p.page_shift) > kPdWhole * kPdKeys;
+}
+
 // The decode's workspace: two partial row sets and one join per CTA of the grid.
 size_t paged_decode_ws_bytes(int sms, int d) {
   return static_cast<size_t>(kPdCtasPerSm * sms) * (2 * kPdRows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
@@ -133,6 +139,7 @@ attn_status_t launch_paged_decode(const PagedDecodeParams& a, int sms, int dev, 
   }
   PdlLaunch l(static_cast<unsigned>(kPdCtasPerSm * sms), kPdThreads, PagedDecodeCfg<D>::kSmemBytes, st);
   if (cudaLaunchKernelEx(&l.cfg, paged_decode_kernel<D>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!paged_can_split(a.p)) return ATTN_OK;
   PdlLaunch j(static_cast<unsigned>(kPdCtasPerSm * sms), kPdRows * 32, 0, st);
   return cudaLaunchKernelEx(&j.cfg, paged_decode_join_kernel<D>, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -175,10 +182,9 @@ attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams&
   }
   PdlLaunch l(static_cast<unsigned>(sms), kPrefillThreads, Cfg::kSmemBytes, st);
   if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
-  const int rows = r.joins != nullptr ? kPdCtasPerSm * sms : 0;
-  PdlLaunch j(static_cast<unsigned>(sms * 2 * (D / 64) + rows), kPdRows * 32, 0, st);
-  return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r, sms, rows) == cudaSuccess ? ATTN_OK
-                                                                                              : ATTN_ERR_CUDA;
+  if (!paged_can_split(a.p)) return ATTN_OK;
+  PdlLaunch j(static_cast<unsigned>(sms), kPdRows * 32, 0, st);
+  return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // 4-D map (d, head in group, KV head, token) over q [T, Hq, d]; box {64, hc, 1, tpt}, 128-byte swizzle.
