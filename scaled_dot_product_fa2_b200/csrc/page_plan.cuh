@@ -60,6 +60,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = 1 << p.page_shift;
   const int64_t cap_keys = static_cast<int64_t>(p.max_pages) << p.page_shift;
+  // a programmatic dependent of what precedes it, and what follows may be one of this kernel
+  grid_dependency_trigger();
+  grid_dependency_wait();
 
   const int raw_head = p.free_range[0], raw_tail = p.free_range[1];
   const int head = min(max(raw_head, 0), p.num_free);

@@ -254,18 +254,20 @@ attn_status_t attn_page_plan(const int* past_lens, const int* new_lens, int* blo
   // one cluster, just wide enough for one pass over the tokens
   int ctas = 1;
   while (ctas < kPlanMaxCluster && static_cast<int64_t>(ctas) * kPlanThreads * kPlanTokens < T) ctas *= 2;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(plan_smem_bytes(B));
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, page_plan_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -306,10 +308,11 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
   prm.page_shift = log2_of(cache->page_size);
   prm.num_pages = cache->num_pages;
   const int grid = static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * kRopeBlocksPerSm));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 128) rope_append_kernel<128, true><<<grid, kRopeWarps * 32, 0, st>>>(prm);
-  else rope_append_kernel<64, true><<<grid, kRopeWarps * 32, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  PdlLaunch l(static_cast<unsigned>(grid), kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream));
+  return (d == 128 ? cudaLaunchKernelEx(&l.cfg, rope_append_kernel<128, true>, prm)
+                   : cudaLaunchKernelEx(&l.cfg, rope_append_kernel<64, true>, prm)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {

@@ -101,6 +101,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
       if (p.total_lens != nullptr) p.total_lens[i] = rope_total_length(__ldg(p.past_lens + i), p.S_new);
   }
 
+  // A programmatic dependent of what precedes it (the page plan, in a step), and what follows may be one
+  // of this kernel.
+  if constexpr (PAGED) {
+    grid_dependency_trigger();
+    grid_dependency_wait();
+  }
   // Token bt's position, or -1 when it is out of range (reported, skipped);
   // its cache row is `row` of batch (or page) b.
   auto token_pos = [&](int bt, int& b, int& t, int& row) {
