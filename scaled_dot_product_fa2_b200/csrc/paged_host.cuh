@@ -307,7 +307,7 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
   prm.slots = slot_map;
   prm.page_shift = log2_of(cache->page_size);
   prm.num_pages = cache->num_pages;
-  const int grid = static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * kRopeBlocksPerSm));
+  const int grid = static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * kRopePagedBlocksPerSm));
   PdlLaunch l(static_cast<unsigned>(grid), kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream));
   return (d == 128 ? cudaLaunchKernelEx(&l.cfg, rope_append_kernel<128, true>, prm)
                    : cudaLaunchKernelEx(&l.cfg, rope_append_kernel<64, true>, prm)) == cudaSuccess

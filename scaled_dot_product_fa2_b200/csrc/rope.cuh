@@ -58,6 +58,7 @@ struct RopeParams {
 constexpr int kRopeWarps = 8;        // warps per block (256 threads)
 constexpr int kRopeUnroll = 3;       // block passes over a token's head rows with loads in flight together
 constexpr int kRopeBlocksPerSm = 4;  // resident blocks per SM
+constexpr int kRopePagedBlocksPerSm = 3;  // the entries read ahead take it over 64 registers
 
 // past + S_new, saturated to the int range instead of wrapping (a corrupt
 // past near INT_MAX gives INT_MAX, which a later decode clamps and reports).
@@ -77,7 +78,7 @@ __global__ void rope_lengths_kernel(const int* past_lens, int* total_lens, int B
 }
 
 template <int D, bool PAGED = false>
-__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
+__global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm : kRopeBlocksPerSm)
     rope_append_kernel(const __grid_constant__ RopeParams p) {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   constexpr int kHalf = D / 2;
@@ -109,11 +110,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
   }
   // Token bt's position, or -1 when it is out of range (reported, skipped);
   // its cache row is `row` of batch (or page) b.
-  auto token_pos = [&](int bt, int& b, int& t, int& row) {
+  // PAGED: from the token's entries (slot, position), read one token earlier.
+  auto token_pos = [&](int bt, int2 entry, int& b, int& t, int& row) {
     if constexpr (PAGED) {
       t = bt;
-      const int slot = __ldg(p.slots + bt);
-      const int pos = __ldg(p.positions + bt);
+      const int slot = entry.x, pos = entry.y;
       b = slot >> p.page_shift;
       row = slot & ((1 << p.page_shift) - 1);
       if (slot < 0) return -1;  // no place: nothing to report
@@ -190,17 +191,33 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocksPerSm)
   // of a block never stop for its stores.
   int bt = blockIdx.x;  // block-uniform
   if (bt >= p.tokens) return;
+  // A paged token's entries are read one token before its rows, and its rows
+  // whether it has a place or not: neither load waits for the other.
+  auto entries = [&](int token) {
+    if constexpr (PAGED) {
+      if (token < p.tokens) return make_int2(__ldg(p.slots + token), __ldg(p.positions + token));
+    }
+    return make_int2(-1, -1);
+  };
   int b, t, row = 0;
-  int pos = token_pos(bt, b, t, row);
   uint4 x[kRopeUnroll];
-  if (pos >= 0) load_rows(bt, 0, x);
+  if constexpr (PAGED) load_rows(bt, 0, x);
+  int pos = token_pos(bt, entries(bt), b, t, row);
+  if constexpr (!PAGED) {
+    if (pos >= 0) load_rows(bt, 0, x);
+  }
+  int2 next = entries(bt + gridDim.x);
   while (true) {
     const int nbt = bt + gridDim.x;
     int nb = 0, nt = 0, nrow = 0, npos = -1;
     uint4 xn[kRopeUnroll];
     if (nbt < p.tokens) {
-      npos = token_pos(nbt, nb, nt, nrow);
-      if (npos >= 0) load_rows(nbt, 0, xn);
+      if constexpr (PAGED) load_rows(nbt, 0, xn);
+      npos = token_pos(nbt, next, nb, nt, nrow);
+      if constexpr (!PAGED) {
+        if (npos >= 0) load_rows(nbt, 0, xn);
+      }
+      next = entries(nbt + gridDim.x);
     }
     if (pos >= 0) {
       const float4* cr = reinterpret_cast<const float4*>(p.cos_t + static_cast<int64_t>(pos) * kHalf + i0);
