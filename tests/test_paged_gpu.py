@@ -588,3 +588,127 @@ def test_many_decodes_in_a_row_over_large_caches(sdpa, page, d):
         if i % 50 >= 47:
             assert torch.equal(o, first[i % 3][0]) and torch.equal(lse, first[i % 3][1])
     sdpa.check_device_error()
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64)])
+def test_lengths_around_what_is_split(sdpa, Hq, Hkv, d):
+    """Tables that hold no more than the keys that stay in one piece, and just more than that."""
+    for L in (128, 255, 256, 257, 320, 384, 385, 513):
+        lens = [L, 1, L - 1]
+        check_decode(sdpa, lens, 1, Hq, Hkv, d, 64, seed=L)
+        bt = Batch([(L, min(L, 70)), (L, 1), (L, L)], Hq, Hkv, d, 64, seed=L)
+        check_fwd(sdpa, bt)
+        exact = -(-L // 64)  # a table without a spare entry
+        bt.table = bt.table[:, :exact].contiguous()
+        check_fwd(sdpa, bt)
+
+
+def test_fwd_of_more_sequences_than_threads(sdpa):
+    rng = random.Random(21)
+    seqs = [(rng.randrange(0, 90), rng.choice((0, 1, 1, 1, 5, 40))) for _ in range(900)]
+    check_fwd(sdpa, Batch(seqs, 4, 2, 64, 32, seed=2, pad=3))
+    check_fwd(sdpa, Batch([(3, 0)] * 500 + [(70, 33)] + [(9, 0)] * 300 + [(40, 1)] + [(0, 0)] * 90, 8, 1, 128, 16))
+
+
+@pytest.mark.parametrize("n", [4, 5, 31, 32, 33, 63, 64, 65, 67, 68, 69, 128, 132, 133])
+def test_fwd_around_the_borders_of_its_tiles(sdpa, n):
+    # 4 heads per KV head: 32 tokens a tile, 64 a unit, 4 left over are the decode's work
+    for L in (n, n + 300):
+        check_fwd(sdpa, Batch([(L, n)], 8, 2, 128, 16, BSHD, seed=n))
+
+
+def test_bad_row_offsets_are_clamped_and_reported(sdpa):
+    bt = Batch([(200, 30), (100, 20), (50, 10)], 8, 2, 128, 64, seed=30)
+    T = bt.T
+    for cu, starts in (([0, 30, 50, T + 7], None), ([-4, 30, 50, T], None)):
+        bt.cu = ints(cu)
+        got = run_fwd(sdpa, bt, BR)
+        reported(sdpa, SEQLEN)
+        check(*got, bt.reference(BR))  # clamped to what it should have been
+    bt.cu = ints([0, 30, 10, T])  # decreasing: no fault, no row outside the batch, and it is told
+    o, lse = sdpa.attn_fwd_paged(bt.q, bt.k, bt.v, bt.cu, bt.seqlens, bt.table)
+    reported(sdpa, SEQLEN)
+    bt.cu = ints([2 ** 31 - 1, -(2 ** 31), 0, 2 ** 31 - 1])
+    sdpa.attn_fwd_paged(bt.q, bt.k, bt.v, bt.cu, bt.seqlens, bt.table)
+    reported(sdpa, SEQLEN)
+
+
+def test_any_workspace_contents_do(sdpa):
+    bt = Batch([(3000, 40), (900, 1), (700, 300)], 8, 2, 128, 16, seed=31)
+    dec = Batch([(L, 2) for L in (1, 5000, 40, 900)], 8, 2, 128, 16, seed=32)
+    ref, dec_ref = bt.reference(BR), dec.reference(BR)
+    ws = sdpa.fwd_paged_workspace(bt.q, bt.k)
+    dec_ws = sdpa.decode_paged_workspace(dec.q.view(4, 2, 8, 128), dec.k)
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        dec_ws.fill_(fill)
+        check(*run_fwd(sdpa, bt, BR, workspace=ws), ref)
+        check(*run_decode(sdpa, dec, 2, BR, workspace=dec_ws), dec_ref)
+    sdpa.check_device_error()
+
+
+def test_two_captured_forwards_share_a_workspace(sdpa):
+    bts = [Batch([(900, 20), (3000 + i, 1), (600, 600)], 8, 2, 128, 16, seed=40 + i) for i in range(2)]
+    refs = [bt.reference(BR) for bt in bts]
+    ws = sdpa.fwd_paged_workspace(bts[0].q, bts[0].k)
+    outs, graphs = [], []
+    for bt in bts:
+        o, lse = torch.zeros_like(bt.q), torch.zeros((8, bt.T), device="cuda")
+        args = (bt.q, bt.k, bt.v, bt.cu, bt.seqlens, bt.table)
+        sdpa.attn_fwd_paged(*args, workspace=ws, out=o, lse=lse)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sdpa.attn_fwd_paged(*args, workspace=ws, out=o, lse=lse)
+        outs.append((o, lse))
+        graphs.append(g)
+    for _ in range(5):
+        for g, (o, lse) in zip(graphs, outs):
+            o.fill_(float("nan"))
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, lse), ref in zip(outs, refs):
+        check(o, lse, ref)
+    sdpa.check_device_error()
+
+
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 128)])
+def test_many_forwards_in_a_row_over_large_caches(sdpa, d, page):
+    """As for the decode: back-to-back calls, whose copies land in any order."""
+    rng = random.Random(d)
+    Hq, Hkv = 32, 8
+    seqs = [(8000, 700)] + [(rng.randrange(1, 8000), 1) for _ in range(24)] + [(5000, 130), (3000, 9)]
+    used = sum(-(-L // page) for L, _ in seqs)
+    T = sum(n for _, n in seqs)
+    sets = []
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    for _ in range(3):
+        k, v = (torch.randn((used, page, Hkv, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+                for _ in range(2))
+        perm = torch.randperm(used, generator=gen, device="cuda").int()
+        table = torch.zeros((len(seqs), -(-8000 // page)), dtype=torch.int32, device="cuda")
+        at = 0
+        for b, (L, _) in enumerate(seqs):
+            m = -(-L // page)
+            table[b, :m] = perm[at:at + m]
+            at += m
+        q = torch.randn((T, Hq, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+        cu = ints([sum(n for _, n in seqs[:b]) for b in range(len(seqs) + 1)])
+        sets.append((q, k, v, cu, ints([L for L, _ in seqs]), table))
+    ws = [sdpa.fwd_paged_workspace(s[0], s[1], BSHD) for s in sets]
+    first = []
+    for s, w in zip(sets, ws):
+        o, lse = sdpa.attn_fwd_paged(*s, layout=BSHD, workspace=w)
+        q, k, v, cu, lens, table = s
+        for b, t in ((0, 0), (0, 699), (3, 702), (25, T - 10)):  # one row's sum, in 64 bits
+            L, n = seqs[b]
+            seen = L - (cu[b + 1].item() - 1 - t)
+            keys = k[table[b, :-(-L // page)].long()].reshape(-1, Hkv, d)[:seen].double()
+            x = torch.einsum("hgd,khd->hgk", q[t].double().view(Hkv, Hq // Hkv, d), keys) / d ** 0.5
+            assert (torch.logsumexp(x, -1).flatten() - lse[:, t].double()).abs().max() < 1e-4, (b, t)
+        first.append((o, lse))
+    for i in range(300):
+        o, lse = sdpa.attn_fwd_paged(*sets[i % 3], layout=BSHD, workspace=ws[i % 3])
+        if i % 50 >= 47:
+            assert torch.equal(o, first[i % 3][0]) and torch.equal(lse, first[i % 3][1])
+    sdpa.check_device_error()
