@@ -19,7 +19,7 @@
 #pragma once
 #include <climits>
 
-#include "ptx.cuh"
+#include "paged_ptx.cuh"
 
 namespace sdpa {
 

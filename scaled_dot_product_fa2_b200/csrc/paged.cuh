@@ -6,11 +6,11 @@
 //     x_j = scale * q . k_j   for visible j,   o = sum_j softmax(x)_j v_j,
 //     lse = ln sum_j exp(x_j),
 // key j being visible iff j < L_b and, under the bottom-right causal mask,
-// j <= i + L_b - n_b.  Keys that are not visible are never read, so whatever a
-// page holds behind a sequence's last key has no effect.
+// j <= i + L_b - n_b.  Whatever a page holds behind a sequence's last key has no
+// effect, infinities and NaN included.
 #pragma once
 #include "fastdiv.h"
-#include "ptx.cuh"
+#include "paged_ptx.cuh"
 
 namespace sdpa {
 

@@ -30,7 +30,7 @@
 #pragma once
 #include <climits>
 
-#include "ptx.cuh"
+#include "paged_ptx.cuh"
 
 namespace sdpa {
 

@@ -1,6 +1,7 @@
 // sdpa_b200.cu -- host side of libsdpa_b200.so: argument checks, TMA
 // descriptors, launch configuration and the extern "C" entry points declared
-// in include/sdpa_b200.h.  Device code lives in prefill.cuh and decode.cuh.
+// in include/sdpa_b200.h.  Device code lives in the .cuh files beside it; the
+// paged cache's host side is paged_host.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
