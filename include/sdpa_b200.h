@@ -435,10 +435,13 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
  * lse = -inf.  Rows behind cu_q[B] are left as they were.  A length outside
  * [0, max_pages * page_size] or a cu_q that decreases or passes T is clamped
  * and reported (ATTN_ERR_SEQLEN); a page id outside [0, num_pages) reads as a
- * page of zeros and is reported (ATTN_ERR_PAGE).
- *   workspace  attn_fwd_paged_workspace_size(...) bytes, device, 16-byte
- *              aligned, caller-owned; nothing in it needs to be initialised,
- *              and calls that may overlap on the GPU need one each.
+ * page of zeros and is reported (ATTN_ERR_PAGE).  What the pages hold behind a
+ * sequence's last key has no effect, NaN included; a NaN or infinity among its
+ * own keys or values may reach every row of that sequence.
+ *   workspace  attn_fwd_paged_workspace_size(...) bytes (about 45 MB, whatever
+ *              the batch), device, 16-byte aligned, caller-owned; nothing in it
+ *              needs to be initialised, and calls that may overlap on the GPU
+ *              need one each.
  * Errors as attn_fwd, plus ATTN_ERR_WORKSPACE and ATTN_ERR_PAGE.
  */
 size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d);
