@@ -398,7 +398,7 @@ typedef struct {
  * tokens end behind T (cu_new is then held at T), or the free pages do not
  * suffice.  A request refused for its pages keeps its tokens' places and
  * positions.  B at most 16384, T at most 2^30.  All pointers 4-byte aligned
- * (16-byte aligned positions and slot_map are written faster).  Errors:
+ * (8-byte aligned positions and slot_map are written faster).  Errors:
  * ATTN_ERR_SHAPE, ATTN_ERR_NULL, ATTN_ERR_ALIGN, ATTN_ERR_PAGE (page_size).
  */
 attn_status_t attn_page_plan(const int* past_lens, const int* new_lens, int* block_table, const int* free_pages,

@@ -39,9 +39,11 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 512;
-constexpr int kPlanTokens = 4;          // consecutive tokens per thread and pass
+constexpr int kPlanTokens = 2;          // consecutive tokens per thread and pass (1: 2.7 / 10.4 us, 2: 3.0 / 8.5,
+                                        // 4: 3.7 / 8.6 for 8 tokens of 8 requests / 40 K tokens of 512)
 constexpr int kPlanMaxBatch = 16384;    // 3 ints of shared memory per request
-constexpr int kPlanMaxCluster = 8;
+constexpr int kPlanMaxCluster = 16;     // with more than kPlanSmallBatch requests 8, the portable size: their CTAs'
+constexpr int kPlanSmallBatch = 4096;   // tables may leave room for one CTA per SM only
 constexpr uint32_t kPlanCap = 1u << 30; // prefix sums saturate here (above every legal total)
 constexpr int kPlanNotGranted = INT_MIN;
 
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   const int ctas = static_cast<int>(gridDim.x);  // one cluster
   if (ctas > 1) cluster_sync();
 
-  const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15u) == 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 7u) == 0;
   const int live = s_cu[p.B];
   const int step = ctas * kPlanThreads * kPlanTokens;
   for (int t0 = (static_cast<int>(blockIdx.x) * kPlanThreads + tid) * kPlanTokens; t0 < p.T; t0 += step) {
@@ -174,8 +176,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
       }
     }
     if (wide && t0 + kPlanTokens <= p.T) {
-      *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int2*>(p.positions + t0) = make_int2(pos[0], pos[1]);
+      *reinterpret_cast<int2*>(p.slots + t0) = make_int2(slot[0], slot[1]);
     } else {
 #pragma unroll
       for (int u = 0; u < kPlanTokens; ++u)

@@ -249,11 +249,15 @@ attn_status_t attn_page_plan(const int* past_lens, const int* new_lens, int* blo
   static std::mutex mu;
   {
     std::lock_guard<std::mutex> lock(mu);
+    if (!smem_done[dev] && cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                               cudaSuccess)
+      return ATTN_ERR_CUDA;
     if (!set_smem(page_plan_kernel, plan_smem_bytes(kPlanMaxBatch), dev, smem_done)) return ATTN_ERR_CUDA;
   }
   // one cluster, just wide enough for one pass over the tokens
   int ctas = 1;
-  while (ctas < kPlanMaxCluster && static_cast<int64_t>(ctas) * kPlanThreads * kPlanTokens < T) ctas *= 2;
+  const int most = B <= kPlanSmallBatch ? kPlanMaxCluster : 8;
+  while (ctas < most && static_cast<int64_t>(ctas) * kPlanThreads * kPlanTokens < T) ctas *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);

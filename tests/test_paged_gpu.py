@@ -712,3 +712,11 @@ def test_many_forwards_in_a_row_over_large_caches(sdpa, d, page):
         if i % 50 >= 47:
             assert torch.equal(o, first[i % 3][0]) and torch.equal(lse, first[i % 3][1])
     sdpa.check_device_error()
+
+
+def test_plan_of_the_largest_batches(sdpa):
+    rng = random.Random(9)
+    for B, hi in ((4096, 12), (4097, 12), (16384, 3)):
+        past = [rng.randrange(300) for _ in range(B)]
+        new = [rng.randrange(hi) for _ in range(B)]
+        check_plan(sdpa, plan_case(past, new, 16, pad=1, seed=B))
