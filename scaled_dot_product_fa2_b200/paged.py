@@ -43,7 +43,7 @@ def _tensor(name, t, dtype, ndim):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-    index = t.get_device() if t.is_cuda else -1
+    index = t.get_device()  # -1: not on a GPU
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -55,7 +55,7 @@ def _ints(name, t, n, index):
     """The address of a contiguous int32 tensor [n] on device `index`."""
     if not _is_tensor(t) or t.dtype is not _INT32 or t.dim() != 1:
         raise TypeError(f"{name} must be an int32 tensor [{n}]")
-    if t.numel() != n or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if t.numel() != n or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor on cuda:{index}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -65,7 +65,7 @@ def _table(t, B, index):
     if not _is_tensor(t) or t.dtype is not _INT32 or t.dim() != 2:
         raise TypeError("block_table must be an int32 tensor [B, max_pages]")
     rows, width = t.shape
-    if rows != B or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if rows != B or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"block_table must be a contiguous [{B}, max_pages] tensor on cuda:{index}")
     return t.data_ptr(), width
 
@@ -73,29 +73,30 @@ def _table(t, B, index):
 def _pages(k_pages, v_pages, layout, index, table=0, max_pages=0):
     """(attn_paged_cache_t as bytes, Hkv, d) of two page pools [N, Hkv, P, d] ([N, P, Hkv, d] for
     LAYOUT_BSHD), dense inside a page and of one stride between pages."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not _is_tensor(t) or t.dtype is not _BF16:
-            raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
-        if not t.is_cuda or t.get_device() != index:
-            raise ValueError(f"{name} must be on cuda:{index}")
+    if not _is_tensor(k_pages) or not _is_tensor(v_pages) or k_pages.dtype is not _BF16 or v_pages.dtype is not _BF16:
+        raise TypeError("k_pages and v_pages must be torch.bfloat16 tensors")
     shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("k_pages and v_pages must have one shape of 4 dims")
+    if k_pages.get_device() != index or v_pages.get_device() != index:
+        raise ValueError(f"k_pages and v_pages must be on cuda:{index}")
     N, s1, s2, d = shape
-    sk, sv = k_pages.stride(), v_pages.stride()
-    dense = (s2 * d, d, 1)
-    if sk[1:] != dense or sv[1:] != dense:
+    stride, s1_stride, s2_stride, s3_stride = strides = k_pages.stride()
+    other = v_pages.stride()
+    if s3_stride != 1 or s2_stride != d or s1_stride != s2 * d or (other != strides and other[1:] != strides[1:]):
         raise ValueError("k_pages and v_pages must be dense inside a page")
-    if v_pages.shape != shape or (N > 1 and sk[0] != sv[0]):
-        raise ValueError("k_pages and v_pages must have one shape and one page stride")
+    if N < 2:
+        stride = 0
+    elif other[0] != stride:
+        raise ValueError("k_pages and v_pages must have one page stride")
     if layout == LAYOUT_BHSD:
         Hkv, P = s1, s2
     elif layout == LAYOUT_BSHD:
         P, Hkv = s1, s2
     else:
         raise ValueError(f"unknown layout {layout}")
-    return _lib.pack_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), table, sk[0] if N > 1 else 0, N, P,
-                                 max_pages, layout), Hkv, d
+    return _lib.pack_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), table, stride, N, P, max_pages,
+                                 layout), Hkv, d
 
 
 def _outputs(q, lse_shape, out, lse, return_lse, index):
@@ -113,7 +114,7 @@ def _outputs(q, lse_shape, out, lse, return_lse, index):
 
 def _workspace(t, index):
     """(address, bytes) of a workspace."""
-    if not _is_tensor(t) or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if not _is_tensor(t) or t.get_device() != index or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous buffer on q's device")
     return t.data_ptr(), t.numel() * t.element_size()
 
