@@ -952,9 +952,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   }
 }
 
-// Join the partials of a unit that crosses shares: a block of 512 threads takes 64 columns of tile t
-// of the unit that begins in CTA c's share; one thread per row and 16 columns, pieces in share order.
-constexpr int kPfJoinCols = 16;
+// Join the partials of a unit that crosses shares: a block of 512 threads takes 32 columns of tile t
+// of the unit that begins in CTA c's share; one thread per row and 8 columns, pieces in share order.
+constexpr int kPfJoinCols = 8;
+constexpr int kPfJoinThreads = 512;
+constexpr int kPfJoinBlocksPerSm = 2;
+static_assert(kPfJoinThreads == 128 * (32 / kPfJoinCols) && kPfJoinThreads == 32 * kPdRows, "a unit's tile, an item's rows");
+static_assert(kPfJoinBlocksPerSm == kPdCtasPerSm, "a block per row share");
 
 template <int D>
 __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta, int t, int col) {
@@ -970,7 +974,7 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
   const int pieces = j0.w - cta + 1;
   auto slot = [&](int s) { return (static_cast<int64_t>(2 * (cta + s) + (s == 0 ? 1 : 0)) * 2 + t) * 128; };
   // one pass with a running maximum, the loads of kAhead pieces at a time
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 3;
   float M = -INFINITY, W = 0.f;
   float acc[kPfJoinCols];
 #pragma unroll
@@ -1014,30 +1018,26 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
         W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
 }
 
-// Both lines' joins in one launch of one block per CTA of the forward, all of which fit on the device
-// at once: they are there when the grid before ends.  Block b looks at the units of shares b, b - 1, ..
-// (part k of share b - k: its tiles and 64-column blocks go to neighbouring blocks) and at the rows of
-// shares 2b and 2b + 1; what has nothing to join costs one look.
+// Both lines' joins in one launch of two blocks per CTA of the forward, all of which fit on the device
+// at once: they are there when the grid before ends.  Blocks 2c and 2c + 1 look at the units of shares c,
+// c - 1, .. (parts 2k and 2k + 1 of share c - k: a unit's tiles and 32-column blocks go to neighbouring
+// blocks), block b at the rows of share b; what has nothing to join costs one look.
 template <int D>
-__global__ void __launch_bounds__(kPdRows * 32) paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a,
-                                                                      const __grid_constant__ PagedDecodeParams d) {
+__global__ void __launch_bounds__(kPfJoinThreads, kPfJoinBlocksPerSm)
+    paged_fwd_join_kernel(const __grid_constant__ PagedFwdParams a, const __grid_constant__ PagedDecodeParams d) {
   grid_dependency_trigger();
-  constexpr int kParts = 2 * (D / 64);
-  const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
-  auto share = [&](int k) { return b >= k ? b - k : b - k + n; };
-  const bool rows = d.joins != nullptr;
+  constexpr int kSteps = D / 32;  // parts (2 tiles, d/32 column blocks) per block of the pair
+  const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x) >> 1;
+  auto share = [&](int k) { return (b >> 1) >= k ? (b >> 1) - k : (b >> 1) - k + n; };
   grid_dependency_wait();
-  unsigned units = 0, items = 0;  // what there is to join
+  unsigned units = 0;  // what there is to join
 #pragma unroll
-  for (int k = 0; k < kParts; ++k) units |= (a.joins[2 * share(k)].w >= 0 ? 1u : 0u) << k;
-#pragma unroll
-  for (int k = 0; k < kPdCtasPerSm; ++k) items |= (rows && d.joins[kPdCtasPerSm * b + k].x >= 0 ? 1u : 0u) << k;
+  for (int k = 0; k < kSteps; ++k) units |= (a.joins[2 * share(k)].w >= 0 ? 1u : 0u) << k;
+  const bool item = d.joins != nullptr && d.joins[b].x >= 0;
 #pragma unroll 1
-  for (int k = 0; k < kParts; ++k)
-    if ((units >> k) & 1u) paged_fwd_join<D>(a, share(k), k & 1, (k >> 1) * 64);
-#pragma unroll 1
-  for (int k = 0; k < kPdCtasPerSm; ++k)
-    if ((items >> k) & 1u) paged_decode_join<D>(d, kPdCtasPerSm * b + k, kPdCtasPerSm * n);
+  for (int k = 0; k < kSteps; ++k)
+    if ((units >> k) & 1u) paged_fwd_join<D>(a, share(k), b & 1, k * 32);
+  if (item) paged_decode_join<D>(d, b, 2 * n);
 }
 
 }  // namespace sdpa

@@ -183,7 +183,7 @@ attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams&
   PdlLaunch l(static_cast<unsigned>(sms), kPrefillThreads, Cfg::kSmemBytes, st);
   if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
   if (!paged_can_split(a.p)) return ATTN_OK;
-  PdlLaunch j(static_cast<unsigned>(sms), kPdRows * 32, 0, st);
+  PdlLaunch j(static_cast<unsigned>(kPfJoinBlocksPerSm * sms), kPfJoinThreads, 0, st);
   return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
