@@ -1,5 +1,5 @@
-// paged_decode.cuh -- split-KV decode attention over a paged KV cache, and the short
-// sequences of the paged forward.
+// paged_decode.cuh -- split-KV decode attention over a paged KV cache, and what
+// the paged forward's units leave of its sequences.
 //
 // A work item is (sequence, KV head, group of up to 16 query rows that share
 // the head); its keys are walked in tiles of 64 with one running maximum,
@@ -26,6 +26,16 @@
 //     leaves an fp32 partial row set per CTA -- at most two per CTA, one for
 //     an item it ends or passes through, one for an item it begins -- and a
 //     second kernel, a programmatic dependent, joins them in share order.
+//     Items of at most kPdWhole tiles stay whole.
+//   * K/V copies are the first to leave the L2 (each is read once): what a
+//     call's start needs, the code above all, stays there.
+// Measured on B200 (d = 128, 32 / 8 heads, three caches in rotation): 8 sequences
+// of 8192 keys 48.1 us = 5.58 TB/s, 64 of 20 to 8192 keys 57.4 us = 5.76 TB/s (85
+// and 88 % of a copy's rate); one of 700 keys 8.8 us, which is the fixed cost of
+// every call: lengths, table entry and first copy one after the other, the merge
+// and the join.  One CTA of eight warps per SM took 136.9 us for the 64 sequences
+// (short items leave the SM idle while they are merged), shares without an item
+// cost 85.
 #pragma once
 #include "decode.cuh"
 #include "paged.cuh"
