@@ -238,7 +238,8 @@ def attn_fwd_paged(q, k_pages, v_pages, cu_q, seqlens_k, block_table, causal: in
         workspace = fwd_paged_workspace(q, k_pages, layout)
     ws, ws_bytes = _workspace(workspace, index)
     _call(_lib.get().attn_fwd_paged, "attn_fwd_paged", index, q.data_ptr(), cache, cu, lens,
-          out.data_ptr(), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, d, scale, causal, ws, ws_bytes)
+          out.data_ptr(), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, d, float(scale),
+          int(causal), ws, ws_bytes)
     return out, lse
 
 
@@ -262,5 +263,5 @@ def attn_decode_splitkv_paged(q, k_pages, v_pages, seqlens_k, block_table, causa
     ws, ws_bytes = _workspace(workspace, index)
     _call(_lib.get().attn_decode_splitkv_paged, "attn_decode_splitkv_paged", index, q.data_ptr(),
           cache, lens, out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, Sq, d,
-          scale, causal, ws, ws_bytes)
+          float(scale), int(causal), ws, ws_bytes)
     return out, lse
