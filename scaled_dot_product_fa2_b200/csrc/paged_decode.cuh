@@ -243,16 +243,13 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
     // for its fixed cost, the others for its tiles
     int64_t xs = sh.prefix * per_seq + static_cast<int64_t>(hr) * (s.T + kPdItemCost);
     int tile = max(0, static_cast<int>(sh.x0 - xs) - kPdItemCost);
-    // the page of this lane's copy of tile `tl`: a table entry, oob_page when it is none, -1 behind the last key
+    // The table entry of this lane's copy of tile `tl`, or nothing (behind the
+    // last key).  It is looked at when the copy is issued, one tile later.
+    auto has_copy = [&](int tl, int len) { return lane < 2 * nb && tl * kPdKeys + (box << pb_shift) < len; };
     auto page_of = [&](int bb, int tl, int len) -> int {
-      const int key = tl * kPdKeys + (box << pb_shift);
-      if (lane >= 2 * nb || key >= len) return -1;
-      int page = __ldg(p.table + static_cast<int64_t>(bb) * p.max_pages + (key >> p.page_shift));
-      if (page < 0 || page >= p.num_pages) {
-        atomicOr(&g_error_word, kErrPage);
-        page = a.oob_page;
-      }
-      return page;
+      return has_copy(tl, len) ? __ldg(p.table + static_cast<int64_t>(bb) * p.max_pages +
+                                       ((tl * kPdKeys + (box << pb_shift)) >> p.page_shift))
+                               : 0;
     };
     int page = page_of(b, tile, s.L);
     while (ok && xs + kPdItemCost < sh.x1) {
@@ -263,6 +260,8 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
                           : static_cast<int>(min(static_cast<int64_t>(s.T), sh.x1 - xs - kPdItemCost)) - tile;
       const bool whole = tile == 0 && n == s.T;
       const int head = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_rg));
+      const int nk = s.L > 0 ? n : 0;
+      if (n > 0) announce(s, hr, tile, nk, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
       {
         // the piece's query rows into the first-level cache
         const int r0 = (hr - head * a.row_groups) * kPdRows;
@@ -280,8 +279,6 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
         join = make_int4(s.tok0, hr, 0, s.cnt);
         join_end = xs + kPdItemCost + s.T;
       }
-      const int nk = s.L > 0 ? n : 0;
-      if (n > 0) announce(s, hr, tile, nk, whole ? -1 : (tile > 0 ? 2 * cta : 2 * cta + 1));
       const int64_t xe = xs + kPdItemCost + s.T;
       const bool more = xe + kPdItemCost < sh.x1;  // the next item has tiles in this share
       int nb2 = b, nhr = hr + 1;
@@ -304,7 +301,7 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
       }
       for (int i = 0; ok && i < nk; ++i) {
         const int tl = tile + i;
-        const int cur = page;
+        const int raw = page;
         if (i + 1 < nk) page = page_of(b, tl + 1, s.L);
         else if (more) page = page_of(nb2, 0, ns.L);
         const int st = issued % NS;
@@ -313,7 +310,12 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
         const int copies = min(nb, (s.L - tl * kPdKeys + pb - 1) >> pb_shift);
         if (lane == 0) mbar_arrive_expect_tx(sm.full(st), 2u * static_cast<uint32_t>(copies) * box_bytes);
         __syncwarp();
-        if (cur >= 0) {
+        if (has_copy(tl, s.L)) {
+          int cur = raw;
+          if (cur < 0 || cur >= p.num_pages) {
+            atomicOr(&g_error_word, kErrPage);
+            cur = a.oob_page;
+          }
           const int row = (tl * kPdKeys + (box << pb_shift)) & ((1 << p.page_shift) - 1);
           tma_load_5d_hint(sm.ring + st * Cfg::kStageBytes + (is_v ? Cfg::kHalfBytes : 0) + box * box_bytes,
                       is_v ? &a.tm_v : &a.tm_k, 0, row, 0, head, cur, sm.full(st), policy);

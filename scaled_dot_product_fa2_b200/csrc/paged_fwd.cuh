@@ -372,15 +372,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       bool ok = true;
       int4 join0 = make_int4(0, 0, 0, -1), join1 = make_int4(0, 0, 0, 0);  // the unit that a later share ends
       int64_t join_last = 0;                                               // its last key tile's place
-      auto page_of = [&](int b, int j, int L) -> int {  // the page of this lane's copy of key tile j
-        const int key = j * 128 + box * pb;
-        if (!copier || key >= L) return a.oob_page;
-        int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift));
-        if (page < 0 || page >= p.num_pages) {
-          atomicOr(&g_error_word, kErrPage);
-          page = a.oob_page;
-        }
-        return page;
+      // The table entry of this lane's copy of key tile j (none behind the last
+      // key).  It is looked at when the copy is issued, one tile later.
+      auto has_copy = [&](int j, int L) { return copier && j * 128 + box * pb < L; };
+      auto page_of = [&](int b, int j, int L) -> int {
+        return has_copy(j, L)
+                   ? __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + ((j * 128 + box * pb) >> p.page_shift))
+                   : 0;
       };
       if (x0 < x1) {
         int b = static_cast<int>(s_first[0]);
@@ -467,8 +465,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
 #pragma unroll 1
             for (int x = 0; ok && x < steps; ++x) {
               const int j = j0 + x;
-              const int cur = page;
+              int cur = page;
               if (x + 1 < steps) page = page_of(b, j + 1, s.L);
+              if (!has_copy(j, s.L)) {
+                cur = a.oob_page;  // rows behind the last key: zeros
+              } else if (cur < 0 || cur >= p.num_pages) {
+                atomicOr(&g_error_word, kErrPage);
+                cur = a.oob_page;
+              }
               const int row = (j * 128 + box * pb) & ((1 << p.page_shift) - 1);
               const bool clean = (j + 1) * 128 > s.L;  // V's rows behind the last key
 #pragma unroll
