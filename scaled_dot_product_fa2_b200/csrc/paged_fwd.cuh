@@ -51,7 +51,7 @@ namespace sdpa {
 // Weights on the line, in proportion to the times above.
 constexpr int kPfPair = 8, kPfThin = 6;   // per key
 constexpr int kPfUnitCost = 1600;
-constexpr float kPfRowPlace = 150.f;      // a place on the short sequences' line: 0.4 us of an SM
+constexpr float kPfRowPlace = 150.f;      // a place on the rows' line
 // Units of this many key tiles or fewer are not split: joining costs more.
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
@@ -82,7 +82,7 @@ struct PagedFwdCfg {
   static constexpr int kRingOffset = (kNumBars * 8 + 15) / 16 * 16;   // pieces: kPfRing x 16 ints
   static constexpr int kMergeOffset = kRingOffset + kPfRing * 64;     // thin units: (max, sum) of tile 1's rows
   static constexpr int kEnd = (2 + NS) * kTileBytes + kMergeOffset + 128 * 8;
-  // a CTA that takes such rows holds two of the decode's CTAs instead
+  // a CTA that takes the rows that the units leave holds two of the decode's CTAs instead
   static constexpr int kRowsBytes = (PagedDecodeCfg<D>::kSumOffset + 1023) / 1024 * 1024;
   // above both: sums of 12 warps and two lines, prefix and first sequence of two shares, TMEM base, abort flag
   static constexpr int kSumOffset = kEnd > 2 * kRowsBytes ? kEnd : 2 * kRowsBytes;
@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
 
   // ---- the two lines, and this CTA's share of one of them
   const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
-  const int per_seq = p.Hkv * a.chunks;  // units' heads; the short sequences have p.Hkv
+  const int per_seq = p.Hkv * a.chunks;  // head tiles per sequence of the units (the rows: p.Hkv)
   int64_t x0 = 0, x1 = 0, total = 0, quot = 0;
   int G = 0, rem = 0;
   auto share_begin = [&](int c) -> int64_t { return quot * c + rem * c / G; };  // floor(total * c / G)
-  int row_ctas = 0;     // the last CTAs of the grid, which take the short sequences
+  int row_ctas = 0;     // the last CTAs of the grid, which take the rows that the units leave
   bool takes_rows = false;
   PdShare sh[2];
   {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
     auto share = [&](const int64_t (&all)[2]) {
       total = all[0] * per_seq;
       const int64_t row_total = all[1] * p.Hkv;
-      // CTAs for the short sequences: in proportion to the two lines' times
+      // CTAs for the rows: in proportion to the two lines' times
       if (row_total > 0) {
         const float wr = static_cast<float>(row_total) * kPfRowPlace, wu = static_cast<float>(total);
         row_ctas = total > 0 ? min(max(static_cast<int>(ctas * wr / (wr + wu) + 0.5f), 1), ctas - 1) : ctas;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
     }
     __syncthreads();
   }
-  // joins that nobody else writes: the units' of a CTA with short sequences, and the reverse
+  // joins that nobody else writes: the units' of a CTA with rows, and the reverse
   if (threadIdx.x < 2) {
     if (takes_rows) a.joins[2 * cta + threadIdx.x] = make_int4(0, 0, 0, -1);
     else if (rows.joins != nullptr) rows.joins[2 * (row_ctas + cta) + threadIdx.x] = make_int4(-1, 0, 0, 0);
