@@ -22,6 +22,9 @@
 //     place from the lengths on the device.  A unit that crosses shares leaves
 //     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
 //     programmatic dependent, joins in share order.
+//   * Cuts cost: partials, a piece more per CTA and the join, 14 us in all.  Where
+//     whole units balance as well or nearly (up to kPfRounds units a CTA, dealt in
+//     the order of their weights there and back), they stay whole.
 //   * What a sequence leaves behind its full units is the decode's work where it
 //     is no more than kRowUnit rows (a single token of up to 16 heads): a 128-row
 //     tile would load the same bytes at a lower rate.  These rows form a line of
@@ -36,8 +39,8 @@
 //     zeroes them in V's last tile before the MMAs may read it.
 // Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 1.90 ms = 1157
 // TFLOP/s at full clocks (the contiguous forward: 1.81), 129 tokens behind 32639
-// keys 94.8 us = 730 TFLOP/s, a 2000-token chunk with 40 single tokens 88.2 us,
-// five prompts of 3 to 150 tokens 12.0 us.  A key step of a pair takes 2.1 us for
+// keys 95.6 us = 723 TFLOP/s, a 2000-token chunk with 40 single tokens 75.0 us,
+// five prompts of 3 to 150 tokens 12.6 us.  A key step of a pair takes 2.1 us for
 // 1.1 us of tensor work: the softmax chain of one row per thread bounds it, as in
 // prefill.cuh.  The weights: at full clocks a step of 128 keys takes 2.1 us in a
 // pair and 1.7 us in a thin unit (its ring of five slots covers one copy's latency
@@ -56,6 +59,13 @@ constexpr float kPfRowPlace = 150.f;      // a place on the rows' line
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
 constexpr int kPfQWarp = 11;     // loads Q; cleans V's last tile
+// Whole units are dealt where that leaves the last CTA at most this much behind a share.  Both sides measured, in us
+// (d = 128): a prompt of 1300 tokens, 32 / 8 heads, 34.2 whole, 41.3 cut; 2000 tokens of 32 heads without sharing 54.0
+// and 67.1; 25 chunks of 185 to 555 tokens, 16 / 2 heads, 79.6 and 88.7; 1024 tokens (4600 behind a share) 29.4 and
+// 34.1; the other way round 256 tokens after 1000 (8300 behind) 33.2 and 24.1, 2000 tokens of 16 / 2 heads (9500
+// behind) 48.1 and 42.6.  To look costs 0.6 us where the answer is no.
+constexpr float kPfJoinCost = 7000.f;
+constexpr int kPfRounds = 16;      // units of a CTA, at most; with more of them a cut weighs little
 
 struct PagedFwdParams {
   PagedParams p;
@@ -66,6 +76,8 @@ struct PagedFwdParams {
   int hc, chunks;     // heads per tile, tiles of heads per group
   int tpt;            // tokens per tile: 128 / hc
   FastDiv div_hc, div_chunks;  // by hc, chunks
+  int can_split;      // whether the table holds enough keys for a unit to be split
+  FastDiv div_per_seq;  // by Hkv * chunks
   float* part_o;      // [2 * CTAs][2 tiles][d][128 rows] locally normalised partial outputs
   float2* part_ml;    // [2 * CTAs][2 tiles][128] (max of scale * q.k, sum)
   int4* joins;        // [CTAs][2] {first token, first head, heads, last CTA (-1: no join)}, {tokens of tile 0, 1, -, -}
@@ -84,9 +96,11 @@ struct PagedFwdCfg {
   static constexpr int kEnd = (2 + NS) * kTileBytes + kMergeOffset + 128 * 8;
   // a CTA that takes the rows that the units leave holds two of the decode's CTAs instead
   static constexpr int kRowsBytes = (PagedDecodeCfg<D>::kSumOffset + 1023) / 1024 * 1024;
-  // above both: sums of 12 warps and two lines, prefix and first sequence of two shares, TMEM base, abort flag
+  // above both: sums of 12 warps and two lines, prefix and first sequence of two shares, whole units, TMEM
+  // base, abort flag
   static constexpr int kSumOffset = kEnd > 2 * kRowsBytes ? kEnd : 2 * kRowsBytes;
-  static constexpr int kSmemBytes = kSumOffset + 28 * 8 + 8;
+  static constexpr int kListOffset = kSumOffset + 28 * 8;  // whole units: {sequence, head tile, unit} each
+  static constexpr int kSmemBytes = kListOffset + (3 * kPfRounds + 1) * 4 + 8;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 };
 
@@ -162,7 +176,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + Cfg::kSumOffset);  // [2 lines][12 warps]
   int64_t* const s_prefix = s_sum + 24;  // [2 shares] weight of the sequences before the first one, per head
   int64_t* const s_first = s_sum + 26;   // [2 shares] that sequence
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_sum + 28);
+  int* const s_list = reinterpret_cast<int*>(smem + Cfg::kListOffset);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_list + 3 * kPfRounds + 1);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // Entries of an announced piece.
   enum { kHead, kG0, kHeads, kTok0, kCnt0, kCnt1, kLim, kKeys, kJ0, kN0, kN1, kThin, kSlot, kSteps };
@@ -233,17 +248,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   auto share_begin = [&](int c) -> int64_t { return quot * c + rem * c / G; };  // floor(total * c / G)
   int row_ctas = 0;     // the last CTAs of the grid, which take the rows that the units leave
   bool takes_rows = false;
+  int whole_units = -1;  // units of this CTA where whole units are dealt
   PdShare sh[2];
   {
     constexpr int kWarps = kPrefillThreads / 32;
-    auto costs_of = [&](int b, int64_t (&t)[2]) {
+    auto costs_of = [&](int b, int64_t (&t)[2]) -> int {  // returns its units
       t[0] = t[1] = 0;
-      if (b >= p.B) return;
+      if (b >= p.B) return 0;
       const PagedSeq q = paged_seq(p, b);
       if (q.bad && cta == 0) atomicOr(&g_error_word, kErrSeqlen);
-      if (q.n == 0) return;
-      t[0] = pf_of(a, q).cost;
+      if (q.n == 0) return 0;
+      const PfSeq s = pf_of(a, q);
+      t[0] = s.cost;
       t[1] = pd_cost(pd_of(p, q));
+      return s.units;
     };
     // inclusive sums over the block's threads and their totals
     auto block_scan = [&](const int64_t (&t)[2], int64_t (&incl)[2], int64_t (&all)[2]) {
@@ -307,12 +325,94 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         s_prefix[0] = end[0] - t[0];
       }
     };
+    // Whole units where they balance: no partials, no join.  A thread takes one unit (of one head tile: all have
+    // the same) and ranks it by weight, counting what is heavier; then they are dealt to the CTAs there and back.
+    // Taken where the heaviest hand is at most kPfJoinCost above a share.  Returns this CTA's number of units (-1:
+    // shares).  Loops are not unrolled: the code runs once, and cold code costs by its length.
+    auto take_whole = [&](int n, int units_before) -> int {
+      const int hands = ctas - row_ctas;
+      const int units = n * per_seq;
+      int* const s_base = reinterpret_cast<int*>(smem + 2 * Cfg::kTileBytes);  // in the K/V slots: [384] first unit
+      float* const s_w = reinterpret_cast<float*>(s_base + kPrefillThreads);   // [384] weights
+      int2* const s_rank = reinterpret_cast<int2*>(s_w + kPrefillThreads);     // [384] (sequence, unit) of each rank
+      float* const s_load = reinterpret_cast<float*>(s_rank + kPrefillThreads);  // [384] hands
+      const int tid = static_cast<int>(threadIdx.x);
+      s_base[tid] = units_before;
+      __syncthreads();
+      int b = 0, v = 0;
+      float w = 0.f;
+      if (tid < n) {
+#pragma unroll 1
+        for (int hi = p.B; hi - b > 1;) {  // the last sequence whose units begin at or before this one
+          const int mid = (b + hi) >> 1;
+          if (s_base[mid] <= tid) b = mid;
+          else hi = mid;
+        }
+        v = tid - s_base[b];
+        const PagedSeq q = paged_seq(p, b);
+        const int t0 = 2 * a.tpt * v, t1 = min(q.n, t0 + 2 * a.tpt);
+        const int keys = paged_visible(p.causal, t1, q.L, p.causal == 2 ? q.L - q.n : 0);
+        w = static_cast<float>(kPfUnitCost + (t1 - t0 > a.tpt ? kPfPair : kPfThin) * static_cast<int64_t>(keys));
+      }
+      s_w[tid] = w;
+      const float most = static_cast<float>(total) + kPfJoinCost * G;  // G times the heaviest hand there may be
+      if (__syncthreads_or(w * G > most)) {
+        fence_async_shared();
+        return -1;
+      }
+      if (tid < n) {
+        int rank = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; j += 4) {  // (behind n: weight 0)
+          const float4 o = *reinterpret_cast<const float4*>(s_w + j);
+          rank += (o.x > w || (o.x == w && j < tid)) + (o.y > w || (o.y == w && j + 1 < tid)) +
+                  (o.z > w || (o.z == w && j + 2 < tid)) + (o.w > w || (o.w == w && j + 3 < tid));
+        }
+        s_rank[rank] = make_int2(b, v);
+        s_load[rank] = w;
+      }
+      __syncthreads();
+      // the k-th unit of hand c
+      auto dealt = [&](int c, int k) { return k * hands + ((k & 1) ? hands - 1 - c : c); };
+      float load = 0.f;
+      int mine = 0;
+      if (tid < hands) {
+#pragma unroll 1
+        for (int k = 0; k < kPfRounds; ++k) {
+          const int u = dealt(tid, k);
+          if (u >= units) break;
+          load += s_load[fastdiv(static_cast<uint32_t>(u), a.div_per_seq)];
+          ++mine;
+        }
+        if (tid == cta) s_list[3 * kPfRounds] = mine;
+      }
+      const int u = tid < kPfRounds ? dealt(cta, tid) : units;
+      if (u < units) {
+        const int i = static_cast<int>(fastdiv(static_cast<uint32_t>(u), a.div_per_seq));
+        s_list[3 * tid] = s_rank[i].x;
+        s_list[3 * tid + 1] = u - i * per_seq;
+        s_list[3 * tid + 2] = s_rank[i].y;
+      }
+      fence_async_shared();  // the space is the K/V copies' from here on
+      return __syncthreads_and(load * G <= most) ? s_list[3 * kPfRounds] : -1;
+    };
     int64_t t[2], incl[2], all[2];
     if (p.B <= kPrefillThreads) {
-      costs_of(threadIdx.x, t);
+      // the number of units rides in the upper bits of the rows' line (384 sequences: the fields do not overflow)
+      constexpr int kShift = 40, kMost = 1 << 14;
+      const int units = costs_of(threadIdx.x, t);
+      t[1] += static_cast<int64_t>(min(units, kMost)) << kShift;
       block_scan(t, incl, all);
+      const int64_t n = all[1] >> kShift;
+      const int before = static_cast<int>((incl[1] - t[1]) >> kShift);
+      for (int64_t* x : {&t[1], &incl[1], &all[1]}) *x &= (int64_t{1} << kShift) - 1;
       share(all);
       find(threadIdx.x, t, incl);
+      // no look at them where there are too many, or where a unit of the mean weight is too heavy
+      const float u = static_cast<float>(n * per_seq);
+      if (a.can_split && !takes_rows && n > 0 && n <= kPrefillThreads && u <= kPfRounds * (ctas - row_ctas) &&
+          static_cast<float>(total) * (G - u) <= kPfJoinCost * G * u)
+        whole_units = take_whole(static_cast<int>(n), before);
     } else {
       int64_t mine[2] = {0, 0}, base[2] = {0, 0};
       for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) {
@@ -380,19 +480,30 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
                    ? __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + ((j * 128 + box * pb) >> p.page_shift))
                    : 0;
       };
+      int dealt = 0;  // whole units begun
+      if (whole_units >= 0) {  // each is its own line, which one share covers
+        x0 = 0;
+        x1 = whole_units > 0 ? int64_t{1} << 60 : 0;
+      }
       if (x0 < x1) {
-        int b = static_cast<int>(s_first[0]);
+        int b = whole_units > 0 ? s_list[0] : static_cast<int>(s_first[0]);
         PfSeq s = pf_seq(a, b);
-        const int64_t in_seq = x0 - s_prefix[0] * per_seq;
-        int hr = static_cast<int>(div64(in_seq, s.cost));   // KV head * chunks + head tile
-        const int64_t in_head = in_seq - hr * s.cost;
-        int v = 0;
-        for (int hi = s.units; hi - v > 1;) {  // last unit that begins at or before the share
-          const int mid = (v + hi) >> 1;
-          if (pf_prefix(a, mid, s.L, s.coff) <= in_head) v = mid;
-          else hi = mid;
+        int hr, v = 0;     // KV head * chunks + head tile, unit
+        int64_t xs = 0;    // where the unit begins
+        if (whole_units > 0) {
+          hr = s_list[1];
+          v = s_list[2];
+        } else {
+          const int64_t in_seq = x0 - s_prefix[0] * per_seq;
+          hr = static_cast<int>(div64(in_seq, s.cost));
+          const int64_t in_head = in_seq - hr * s.cost;
+          for (int hi = s.units; hi - v > 1;) {  // last unit that begins at or before the share
+            const int mid = (v + hi) >> 1;
+            if (pf_prefix(a, mid, s.L, s.coff) <= in_head) v = mid;
+            else hi = mid;
+          }
+          xs = x0 - in_head + pf_prefix(a, v, s.L, s.coff);
         }
-        int64_t xs = x0 - in_head + pf_prefix(a, v, s.L, s.coff);  // where the unit begins
         while (ok && xs < x1) {
           // unit (b, hr, v): tokens v tu .. of the sequence
           const int cnt0 = min(s.n - v * tu, a.tpt);
@@ -500,6 +611,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
             ++ui;
           }
           // the unit behind this one
+          if (whole_units > 0) {
+            if (++dealt == whole_units) break;
+            b = s_list[3 * dealt];
+            hr = s_list[3 * dealt + 1];
+            v = s_list[3 * dealt + 2];
+            s = pf_seq(a, b);
+            continue;
+          }
           xs = xe;
           if (++v == s.units) {
             v = 0;

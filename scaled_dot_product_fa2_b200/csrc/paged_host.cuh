@@ -348,6 +348,9 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, con
   a.p.unit_tokens = 2 * a.tpt;
   a.p.div_tu = make_fastdiv(static_cast<uint32_t>(a.p.unit_tokens));
   a.div_chunks = make_fastdiv(static_cast<uint32_t>(a.chunks));
+  if (static_cast<int64_t>(Hkv) * a.chunks > INT_MAX / 2) return ATTN_ERR_SHAPE;
+  a.div_per_seq = make_fastdiv(static_cast<uint32_t>(Hkv * a.chunks));
+  a.can_split = paged_can_split(a.p) ? 1 : 0;
   const bool pages = a.p.num_pages > 0;
   a.oob_page = std::max(a.p.num_pages, 1);
   const int box = std::min(1 << a.p.page_shift, 128);

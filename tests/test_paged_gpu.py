@@ -617,6 +617,22 @@ def test_fwd_around_the_borders_of_its_tiles(sdpa, n):
         check_fwd(sdpa, Batch([(L, n)], 8, 2, 128, 16, BSHD, seed=n))
 
 
+@pytest.mark.parametrize("seqs,Hq,Hkv,d,causal", [
+    ([(700, 700)] * 13, 8, 2, 128, BR),                           # 286 equal units in all: two each and a rest
+    ([(1300, 1300)], 32, 8, 128, BR),                             # one prompt, units of every weight
+    ([(1300, 1300)], 32, 8, 64, NONE),
+    ([(900 - 37 * i, 300 - 13 * i) for i in range(20)] + [(0, 0), (5, 0), (0, 9)], 8, 2, 64, BR),
+    ([(100 * i, 90 + i) for i in range(24)], 16, 2, 128, TL),     # ends in one tile, rows that see nothing
+    ([(600, 16 * 24 * 2)], 128, 1, 64, BR),                       # a unit per thread that ranks them, and one more
+    ([(600, 16 * 24 * 2 + 2)], 128, 1, 64, BR),
+    ([(700, 379)] * 24 + [(300, 256)], 64, 8, 64, BR),            # 16 units a processor on 148, and more
+    ([(700, 379)] * 24 + [(300, 290)], 64, 8, 64, BR),
+    ([(400, 400)] * 3 + [(500 + 7 * i, 1) for i in range(30)], 32, 8, 128, BR),
+])
+def test_fwd_of_units_that_are_dealt_whole(sdpa, seqs, Hq, Hkv, d, causal):
+    check_fwd(sdpa, Batch(seqs, Hq, Hkv, d, 64, BSHD, seed=len(seqs) + d, pad=1), causal)
+
+
 def test_bad_row_offsets_are_clamped_and_reported(sdpa):
     bt = Batch([(200, 30), (100, 20), (50, 10)], 8, 2, 128, 64, seed=30)
     T = bt.T
