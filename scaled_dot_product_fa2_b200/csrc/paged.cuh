@@ -68,6 +68,18 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   return s;
 }
 
+// Asks for the lengths and the table (a line per thread of the grid) while the grid before still runs: into the L2,
+// where what that grid writes of them arrives as well.  64 caches of 20 to 8192 keys 58.1 -> 57.8 us, 129 tokens
+// behind 32639 keys 95.9 -> 95.1.
+__device__ __forceinline__ void paged_warm(const PagedParams& p) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 32;
+  if (i < static_cast<int64_t>(p.B) * p.max_pages) prefetch_l2(p.table + i);
+  if (i < p.B) {
+    prefetch_l2(p.lens + i);
+    if (p.cu_q != nullptr) prefetch_l2(p.cu_q + i);
+  }
+}
+
 // a / b of non-negative values, by the 32-bit division where both fit.
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);

@@ -633,13 +633,15 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm) paged_decode_kernel(
     sm.init();
     s_first = s_prefix = 0;
   }
+  paged_warm(p);
   if (warp == kPdWarps && lane == 0) {
     tma_prefetch_desc(&a.tm_k);
     tma_prefetch_desc(&a.tm_v);
   }
   __syncthreads();
   // Launched as a programmatic dependent of whatever precedes it on the stream:
-  // no global memory is touched before this wait.
+  // no global memory is read or written before this wait (the lines asked for above go
+  // to the L2 only).
   grid_dependency_wait();
   grid_dependency_trigger();
 

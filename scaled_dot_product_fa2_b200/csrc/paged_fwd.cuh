@@ -39,7 +39,7 @@
 //     zeroes them in V's last tile before the MMAs may read it.
 // Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 1.90 ms = 1157
 // TFLOP/s at full clocks (the contiguous forward: 1.81), 129 tokens behind 32639
-// keys 95.6 us = 723 TFLOP/s, a 2000-token chunk with 40 single tokens 75.0 us,
+// keys 95.1 us = 727 TFLOP/s, a 2000-token chunk with 40 single tokens 75.0 us,
 // five prompts of 3 to 150 tokens 12.6 us.  A key step of a pair takes 2.1 us for
 // 1.1 us of tensor work: the softmax chain of one row per thread bounds it, as in
 // prefill.cuh.  The weights: at full clocks a step of 128 keys takes 2.1 us in a
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  paged_warm(p);
   if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&a.tm_q);
     tma_prefetch_desc(&a.tm_k);
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // Launched as a programmatic dependent of whatever precedes it on the stream:
-  // no global memory is touched before this wait.
+  // no global memory is read or written before this wait (the lines asked for above go
+  // to the L2 only).
   grid_dependency_wait();
   grid_dependency_trigger();
 
