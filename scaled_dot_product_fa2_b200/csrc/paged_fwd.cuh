@@ -40,7 +40,7 @@
 // Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 1.90 ms = 1157
 // TFLOP/s at full clocks (the contiguous forward: 1.81), 129 tokens behind 32639
 // keys 95.1 us = 727 TFLOP/s, a 2000-token chunk with 40 single tokens 75.0 us,
-// five prompts of 3 to 150 tokens 12.6 us.  A key step of a pair takes 2.1 us for
+// five prompts of 3 to 150 tokens 11.9 us.  A key step of a pair takes 2.1 us for
 // 1.1 us of tensor work: the softmax chain of one row per thread bounds it, as in
 // prefill.cuh.  The weights: at full clocks a step of 128 keys takes 2.1 us in a
 // pair and 1.7 us in a thin unit (its ring of five slots covers one copy's latency
@@ -76,7 +76,6 @@ struct PagedFwdParams {
   int hc, chunks;     // heads per tile, tiles of heads per group
   int tpt;            // tokens per tile: 128 / hc
   FastDiv div_hc, div_chunks;  // by hc, chunks
-  int can_split;      // whether the table holds enough keys for a unit to be split
   FastDiv div_per_seq;  // by Hkv * chunks
   float* part_o;      // [2 * CTAs][2 tiles][d][128 rows] locally normalised partial outputs
   float2* part_ml;    // [2 * CTAs][2 tiles][128] (max of scale * q.k, sum)
@@ -145,7 +144,9 @@ __device__ __forceinline__ PfSeq pf_of(const PagedFwdParams& a, const PagedSeq& 
 
 __device__ __forceinline__ PfSeq pf_seq(const PagedFwdParams& a, int b) { return pf_of(a, paged_seq(a.p, b)); }
 
-template <int D, int NS>
+// SPLIT: whether units can be split at all, i.e. the table holds more keys than stay whole. Without the code for
+// it five short prompts take 11.9 us instead of 12.6, 40 of 10 to 200 tokens 32.4 instead of 33.6.
+template <int D, int NS, bool SPLIT>
 __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __grid_constant__ PagedFwdParams a,
                                                                        const __grid_constant__ PagedDecodeParams rows) {
   using Cfg = PagedFwdCfg<D, NS>;
@@ -410,11 +411,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       for (int64_t* x : {&t[1], &incl[1], &all[1]}) *x &= (int64_t{1} << kShift) - 1;
       share(all);
       find(threadIdx.x, t, incl);
-      // no look at them where there are too many, or where a unit of the mean weight is too heavy
-      const float u = static_cast<float>(n * per_seq);
-      if (a.can_split && !takes_rows && n > 0 && n <= kPrefillThreads && u <= kPfRounds * (ctas - row_ctas) &&
-          static_cast<float>(total) * (G - u) <= kPfJoinCost * G * u)
-        whole_units = take_whole(static_cast<int>(n), before);
+      if constexpr (SPLIT) {
+        // no look at them where there are too many, or where a unit of the mean weight is too heavy
+        const float u = static_cast<float>(n * per_seq);
+        if (!takes_rows && n > 0 && n <= kPrefillThreads && u <= kPfRounds * (ctas - row_ctas) &&
+            static_cast<float>(total) * (G - u) <= kPfJoinCost * G * u)
+          whole_units = take_whole(static_cast<int>(n), before);
+      }
     } else {
       int64_t mine[2] = {0, 0}, base[2] = {0, 0};
       for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) {
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
     __syncthreads();
   }
   // joins that nobody else writes: the units' of a CTA with rows, and the reverse
-  if (threadIdx.x < 2) {
+  if (SPLIT && threadIdx.x < 2) {
     if (takes_rows) a.joins[2 * cta + threadIdx.x] = make_int4(0, 0, 0, -1);
     else if (rows.joins != nullptr) rows.joins[2 * (row_ctas + cta) + threadIdx.x] = make_int4(-1, 0, 0, 0);
   }
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           const int64_t xe = xs + kPfUnitCost + static_cast<int64_t>(w / 128) * keys;
           if (j1 > j0 || (n_u == 0 && xs >= x0)) {
             const int steps = j1 - j0;
-            const bool whole = steps == n_u;
+            const bool whole = !SPLIT || steps == n_u;
             const int hk = static_cast<int>(fastdiv(static_cast<uint32_t>(hr), a.div_chunks));
             const int chunk = hr - hk * a.chunks;
             const int g0 = chunk * a.hc;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
               n0 = min(max(n_0 - j0, 0), steps);
               n1 = steps;
             }
-            if (j0 == 0 && !whole) {
+            if (SPLIT && j0 == 0 && !whole) {
               join0 = make_int4(tok0, hk * p.group + g0, heads, 0);
               join1 = make_int4(cnt0, cnt1, 0, 0);
               join_last = xs + kPfUnitCost + static_cast<int64_t>(n_u - 1) * w;
@@ -639,12 +642,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           }
         }
       }
-      if (join0.w >= 0) {  // the CTA whose share holds that place
+      if (SPLIT && join0.w >= 0) {  // the CTA whose share holds that place
         int c = static_cast<int>(div64(join_last, quot + 1));  // at most the right one
         while (c + 1 < G && share_begin(c + 1) <= join_last) ++c;
         join0.w = c;
       }
-      if (lane == 0) {
+      if (SPLIT && lane == 0) {
         a.joins[2 * cta] = join0;
         a.joins[2 * cta + 1] = join1;
       }
@@ -996,7 +999,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           for (int i = 0; i < 16; ++i) f[i] = make_float2(0.f, 0.f);
         }
       };
-      if (!idle && slot < 0) {
+      if (!idle && (!SPLIT || slot < 0)) {
         const int g4 = lane & 3;
         uint16_t* dst[4];  // rows of this lane's group of four
 #pragma unroll
@@ -1051,7 +1054,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         if (live && p.lse != nullptr)
           p.lse[static_cast<int64_t>(row_head) * p.T + row_tok] =
               empty_row ? -INFINITY : (m_used * p.scale + lg2_approx(l) * 0.69314718055994531f);
-      } else if (!idle) {
+      } else if (SPLIT && !idle) {
         // a partial: columns outermost, so that a warp writes 32 rows side by side
         float* const dst = a.part_o + (static_cast<int64_t>(slot) * 2 + t) * (D * 128) + r_in_tile;
 #pragma unroll 1

@@ -164,9 +164,9 @@ size_t paged_units_ws_bytes(int sms, int d) {
                                      2 * sizeof(int4));
 }
 
-template <int D, int NS>
-attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams& r, int sms, int dev,
-                               cudaStream_t st) {
+template <int D, int NS, bool SPLIT>
+attn_status_t launch_paged_fwd_split(const PagedFwdParams& a, const PagedDecodeParams& r, int sms, int dev,
+                                     cudaStream_t st) {
   static bool smem_done[kMaxDevices] = {};
   static std::mutex mu;
   using Cfg = PagedFwdCfg<D, NS>;
@@ -175,16 +175,23 @@ attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams&
     if (!smem_done[dev]) {
       // the register split (setmaxnreg) adds up to this launch allocation, as in launch_prefill
       cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, paged_fwd_kernel<D, NS>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+      if (cudaFuncGetAttributes(&fa, paged_fwd_kernel<D, NS, SPLIT>) != cudaSuccess || fa.numRegs != kLaunchRegs)
         return ATTN_ERR_CUDA;
     }
-    if (!set_smem(paged_fwd_kernel<D, NS>, Cfg::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
+    if (!set_smem(paged_fwd_kernel<D, NS, SPLIT>, Cfg::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
   }
   PdlLaunch l(static_cast<unsigned>(sms), kPrefillThreads, Cfg::kSmemBytes, st);
-  if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (!paged_can_split(a.p)) return ATTN_OK;
+  if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS, SPLIT>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!SPLIT) return ATTN_OK;
   PdlLaunch j(static_cast<unsigned>(kPfJoinBlocksPerSm * sms), kPfJoinThreads, 0, st);
   return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, int NS>
+attn_status_t launch_paged_fwd(const PagedFwdParams& a, const PagedDecodeParams& r, int sms, int dev,
+                               cudaStream_t st) {
+  return paged_can_split(a.p) ? launch_paged_fwd_split<D, NS, true>(a, r, sms, dev, st)
+                              : launch_paged_fwd_split<D, NS, false>(a, r, sms, dev, st);
 }
 
 // 4-D map (d, head in group, KV head, token) over q [T, Hq, d]; box {64, hc, 1, tpt}, 128-byte swizzle.
@@ -350,7 +357,6 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, con
   a.div_chunks = make_fastdiv(static_cast<uint32_t>(a.chunks));
   if (static_cast<int64_t>(Hkv) * a.chunks > INT_MAX / 2) return ATTN_ERR_SHAPE;
   a.div_per_seq = make_fastdiv(static_cast<uint32_t>(Hkv * a.chunks));
-  a.can_split = paged_can_split(a.p) ? 1 : 0;
   const bool pages = a.p.num_pages > 0;
   a.oob_page = std::max(a.p.num_pages, 1);
   const int box = std::min(1 << a.p.page_shift, 128);
