@@ -399,44 +399,44 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       fence_async_shared();  // the space is the K/V copies' from here on
       return __syncthreads_and(load * G <= most) ? s_list[3 * kPfRounds] : -1;
     };
-    int64_t t[2], incl[2], all[2];
-    if (p.B <= kPrefillThreads) {
-      // the number of units rides in the upper bits of the rows' line (384 sequences: the fields do not overflow)
-      constexpr int kShift = 40, kMost = 1 << 14;
-      const int units = costs_of(threadIdx.x, t);
+    // 384 sequences at a time: once where that is all of them, else a round for the totals and one for the share.
+    // The number of units rides in the upper bits of the rows' line (the fields of 384 sequences do not overflow).
+    constexpr int kShift = 40, kMost = 1 << 14;
+    int64_t base[2] = {0, 0};
+    bool shared = false;
+#pragma unroll 1
+    for (int b0 = 0;;) {
+      int64_t t[2], incl[2], all[2];
+      const int units = costs_of(b0 + static_cast<int>(threadIdx.x), t);
       t[1] += static_cast<int64_t>(min(units, kMost)) << kShift;
       block_scan(t, incl, all);
-      const int64_t n = all[1] >> kShift;
+      const int n = static_cast<int>(all[1] >> kShift);
       const int before = static_cast<int>((incl[1] - t[1]) >> kShift);
       for (int64_t* x : {&t[1], &incl[1], &all[1]}) *x &= (int64_t{1} << kShift) - 1;
-      share(all);
-      find(threadIdx.x, t, incl);
-      if constexpr (SPLIT) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        incl[q] += base[q];
+        base[q] += all[q];
+      }
+      b0 += kPrefillThreads;
+      const bool first = !shared;
+      if (first && b0 >= p.B) {
+        share(base);
+        shared = true;
+      }
+      if (shared && !(first && p.B > kPrefillThreads)) find(b0 - kPrefillThreads + static_cast<int>(threadIdx.x), t, incl);
+      if (SPLIT && p.B <= kPrefillThreads && !takes_rows && n > 0 && n <= kPrefillThreads) {
         // no look at them where there are too many, or where a unit of the mean weight is too heavy
-        const float u = static_cast<float>(n * per_seq);
-        if (!takes_rows && n > 0 && n <= kPrefillThreads && u <= kPfRounds * (ctas - row_ctas) &&
-            static_cast<float>(total) * (G - u) <= kPfJoinCost * G * u)
-          whole_units = take_whole(static_cast<int>(n), before);
+        const float u = static_cast<float>(n) * per_seq;
+        if (u <= kPfRounds * (ctas - row_ctas) && static_cast<float>(total) * (G - u) <= kPfJoinCost * G * u)
+          whole_units = take_whole(n, before);
       }
-    } else {
-      int64_t mine[2] = {0, 0}, base[2] = {0, 0};
-      for (int b = threadIdx.x; b < p.B; b += kPrefillThreads) {
-        costs_of(b, t);
-        mine[0] += t[0];
-        mine[1] += t[1];
+      if (b0 >= p.B) {
+        if (!first || p.B <= kPrefillThreads || x0 >= x1) break;  // block-uniform
+        b0 = 0;
+        base[0] = base[1] = 0;
       }
-      block_scan(mine, incl, all);
-      share(all);
-      for (int b0 = 0; b0 < p.B && x0 < x1; b0 += kPrefillThreads) {  // block-uniform
-        const int b = b0 + static_cast<int>(threadIdx.x);
-        costs_of(b, t);
-        __syncthreads();  // s_sum's previous contents are read
-        block_scan(t, incl, all);
-        const int64_t end[2] = {base[0] + incl[0], base[1] + incl[1]};
-        find(b, t, end);
-        base[0] += all[0];
-        base[1] += all[1];
-      }
+      __syncthreads();  // s_sum's contents are read
     }
     if (takes_rows && threadIdx.x == 0) {
       // the space becomes that of two decode CTAs
