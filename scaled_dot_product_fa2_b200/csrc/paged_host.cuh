@@ -104,8 +104,8 @@ bool make_page_map(CUtensorMap* map, const void* base, const PagedParams& p, int
 // A launch as a programmatic dependent of what precedes it on the stream.
 struct PdlLaunch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  PdlLaunch(unsigned grid, int threads, int smem, cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  PdlLaunch(unsigned grid, int threads, int smem, cudaStream_t st, unsigned cluster = 1) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(grid);
@@ -114,6 +114,12 @@ struct PdlLaunch {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cluster > 1) {
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = cluster;
+      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+    }
   }
 };
 
@@ -180,10 +186,11 @@ attn_status_t launch_paged_fwd_split(const PagedFwdParams& a, const PagedDecodeP
     }
     if (!set_smem(paged_fwd_kernel<D, NS, SPLIT>, Cfg::kSmemBytes, dev, smem_done)) return ATTN_ERR_CUDA;
   }
-  PdlLaunch l(static_cast<unsigned>(sms), kPrefillThreads, Cfg::kSmemBytes, st);
+  const int ctas = sms & ~1;
+  PdlLaunch l(static_cast<unsigned>(ctas), kPrefillThreads, Cfg::kSmemBytes, st, 2);
   if (cudaLaunchKernelEx(&l.cfg, paged_fwd_kernel<D, NS, SPLIT>, a, r) != cudaSuccess) return ATTN_ERR_CUDA;
   if (!SPLIT) return ATTN_OK;
-  PdlLaunch j(static_cast<unsigned>(kPfJoinBlocksPerSm * sms), kPfJoinThreads, 0, st);
+  PdlLaunch j(static_cast<unsigned>(kPfJoinBlocksPerSm * ctas), kPfJoinThreads, 0, st);
   return cudaLaunchKernelEx(&j.cfg, paged_fwd_join_kernel<D>, a, r) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
