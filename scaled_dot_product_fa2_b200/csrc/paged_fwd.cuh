@@ -42,8 +42,8 @@
 //     zeroes them in V's last tile before the MMAs may read it.
 // Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 1.90 ms = 1157
 // TFLOP/s at full clocks (the contiguous forward: 1.81), 129 tokens behind 32639
-// keys 95.1 us = 727 TFLOP/s, a 2000-token chunk with 40 single tokens 75.0 us,
-// five prompts of 3 to 150 tokens 11.9 us.  A key step of a pair takes 2.1 us for
+// keys 88.9 us = 777 TFLOP/s, a 2000-token chunk with 40 single tokens 69.0 us,
+// five prompts of 3 to 150 tokens 11.7 us.  A key step of a pair takes 2.1 us for
 // 1.1 us of tensor work: the softmax chain of one row per thread bounds it, as in
 // prefill.cuh.  The weights: at full clocks a step of 128 keys takes 2.1 us in a
 // pair and 1.7 us in a thin unit (its ring of five slots covers one copy's latency
@@ -57,7 +57,7 @@ namespace sdpa {
 // Weights on the line, in proportion to the times above.
 constexpr int kPfPair = 8, kPfThin = 6;   // per key
 constexpr int kPfUnitCost = 1600;
-constexpr float kPfRowPlace = 150.f;      // a place on the rows' line
+constexpr float kPfRowPlace = 165.f;      // a place on the rows' line: 0.34 us of an SM
 // Units of this many key tiles or fewer are not split: joining costs more.
 constexpr int kPfWholePair = 2, kPfWholeThin = 4;
 constexpr int kPfRing = 4;         // pieces announced ahead
