@@ -50,6 +50,7 @@
 // per two tiles), a unit 3.2 us besides (first S, last P.V, stores).
 #pragma once
 #include "paged_decode.cuh"
+#include "piece_steps.h"
 #include "prefill.cuh"
 
 namespace sdpa {
@@ -733,87 +734,62 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       __syncwarp();
     } else {
       // ---------------------------------------------- MMA issuer of tile t
-      // As in prefill.cuh; in a thin piece tile t takes key tiles t, t + 2, ...
-      // and releases their slots for both issuers.
+      // The two issuers' products as in prefill.cuh, in the order of piece_steps.h.
       const int t = (warp == kMmaWarp) ? 0 : 1;
       if (lane == 0) {
         const uint64_t hi = static_cast<uint64_t>(sdesc_hi(1024)) << 32;
         const uint64_t dq = hi | sdesc_lo(sQ + t * Cfg::kTileBytes, 16);
         auto dk = [&](int slot) { return hi | sdesc_lo(sKV + slot * Cfg::kTileBytes, 16); };
         auto dv = [&](int slot) { return hi | sdesc_lo(sKV + slot * Cfg::kTileBytes, Cfg::kBlockBytes); };
-        const uint32_t tS = tmem + t * 128;
-        const uint32_t tO = tmem + 2 * 128 + t * D;
-        int it_base = 0, seg = 0, pj = 0, ui = 0;
+        // The operations of walk_piece (piece_steps.h, with the order of the waits and its reason).
+        struct Ops {
+          const decltype(kv_full)& full;
+          const decltype(kv_empty)& empty;
+          const decltype(dk)& k_desc;
+          const decltype(dv)& v_desc;
+          uint32_t p_bar, turn_bar, other_turn, s_bar, o_bar, q_bar, tS, tO;
+          uint64_t dq;
+          volatile int* abort_flag;
+          int nt, pj;
+          __device__ __forceinline__ bool p_ready() { return mbar_wait(p_bar, pj & 1, abort_flag); }
+          __device__ __forceinline__ bool turn_ready(int s) { return mbar_wait(turn_bar, s & 1, abort_flag); }
+          __device__ __forceinline__ bool tile_ready(int i) { return mbar_wait(full(i % NS), (i / NS) & 1, abort_flag); }
+          __device__ __forceinline__ void multiply(int k, int v, int kt) {
+            tc_fence_after();
+            if (k >= 1 && k - 1 < nt) {
+              const uint64_t vd = v_desc(v % NS);
+              issue_pv<D, 0>(tO, tS, vd, k > 1);
+              issue_pv<D, 1>(tO, tS, vd, true);
+              ++pj;
+              if (k == nt) mma_commit(o_bar);
+            }
+            if (k < nt) {
+              issue_qk<D>(tS, dq, k_desc(kt % NS));
+              mma_commit(s_bar);
+              if (k == nt - 1) mma_commit(q_bar);
+            }
+          }
+          __device__ __forceinline__ void free_tile(int i, int times) {
+            mma_commit(empty(i % NS));
+            if (times > 1) mma_commit(empty(i % NS));
+          }
+          __device__ __forceinline__ void hand_over() { mbar_arrive(other_turn); }
+        };
+        Ops op = {kv_full,  kv_empty, dk, dv, p_full(t), turn(t), turn(1 - t), s_full(t), o_full(t), q_empty(t),
+                  tmem + t * 128, tmem + 2 * 128 + t * D, dq, abort_flag, 0, 0};
+        int it_base = 0, seg = 0, ui = 0;
         bool ok = true;
 #pragma unroll 1
         for (int r = 0; ok; ++r) {
           volatile int* const e = next_piece(r, ok);
           if (e == nullptr) break;
-          const int n0 = e[kN0], n1 = e[kN1], steps = e[kSteps];
-          const bool thin = e[kThin] != 0;
+          const PieceSteps steps = {e[kN0], e[kN1], e[kThin] != 0, it_base};
+          it_base += 2 * e[kSteps];
           release(r);
-          const int nt = t ? n1 : n0;
-          const int n_max = max(n0, n1);
-          const int n_slots = thin ? nt : n_max;  // key tiles whose slots this thread releases
+          op.nt = t ? steps.n1 : steps.n0;
           if (!mbar_wait(q_full(t), ui & 1, abort_flag)) break;
-          if (nt == 0) mma_commit(q_empty(t));
-#pragma unroll 1
-          for (int k = 0; k <= n_max; ++k, ++seg) {
-            int slot_v = -1, slot_k = -1;
-            if (k >= 1 && k <= n_slots) {
-              const int x = thin ? 2 * (k - 1) + t : k - 1;
-              const int itv = it_base + 2 * x + 1;
-              slot_v = itv % NS;
-              if (!mbar_wait(kv_full(slot_v), (itv / NS) & 1, abort_flag) ||
-                  (k - 1 < nt && !mbar_wait(p_full(t), pj & 1, abort_flag))) {
-                ok = false;
-                break;
-              }
-            }
-            if (k < n_slots) {
-              const int x = thin ? 2 * k + t : k;
-              const int itk = it_base + 2 * x;
-              slot_k = itk % NS;
-              if (!mbar_wait(kv_full(slot_k), (itk / NS) & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-            }
-            if (t == 1) {
-              if (!mbar_wait(turn(1), seg & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-            } else if (seg >= 1) {
-              if (!mbar_wait(turn(0), (seg - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-            }
-            tc_fence_after();
-            if (k >= 1 && k - 1 < nt) {
-              const uint64_t v_desc = dv(slot_v);
-              issue_pv<D, 0>(tO, tS, v_desc, k > 1);
-              issue_pv<D, 1>(tO, tS, v_desc, true);
-              ++pj;
-              if (k == nt) mma_commit(o_full(t));
-            }
-            if (k < nt) {
-              issue_qk<D>(tS, dq, dk(slot_k));
-              mma_commit(s_full(t));
-              if (k == nt - 1) mma_commit(q_empty(t));
-            }
-            if (slot_v >= 0) {
-              mma_commit(kv_empty(slot_v));
-              if (thin) mma_commit(kv_empty(slot_v));
-            }
-            if (slot_k >= 0) {
-              mma_commit(kv_empty(slot_k));
-              if (thin) mma_commit(kv_empty(slot_k));
-            }
-            mbar_arrive(turn(1 - t));
-          }
-          it_base += 2 * steps;
+          if (op.nt == 0) mma_commit(q_empty(t));
+          ok = walk_piece(op, steps, t, seg);
           ++ui;
         }
         mma_commit(drain);
