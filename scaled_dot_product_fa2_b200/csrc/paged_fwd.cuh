@@ -186,19 +186,27 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // Entries of an announced piece.
   enum { kHead, kG0, kHeads, kTok0, kCnt0, kCnt1, kLim, kKeys, kJ0, kN0, kN1, kThin, kSlot, kSteps };
-  // The r-th piece of this CTA: waits for it; nullptr where there is none left.
-  // The caller's whole warp (or its lone thread) calls it and releases it with
-  // `release` when it has read what it needs.
+  // The r-th piece of this CTA, for a whole warp: waits for it; nullptr where there is none left.  The warp
+  // gives it back with `release` when each of its lanes has read what it needs: the producer may write the
+  // entry again from then on.  The lanes meet in both, since a spin-wait leaves them in any order.
   auto next_piece = [&](int r, bool& ok) -> volatile int* {
     const int k = r % kPfRing;
-    ok = ok && mbar_wait(unit_full(k), (r / kPfRing) & 1, abort_flag);
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(unit_full(k), (r / kPfRing) & 1, abort_flag));
     volatile int* const e = ring + 16 * k;
     return ok && e[kHead] >= 0 ? e : nullptr;
   };
   auto release = [&](int r) {
-    __syncwarp(__activemask());
-    if ((threadIdx.x & 31) == 0 || __activemask() == 1u) mbar_arrive(unit_empty(r % kPfRing));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(unit_empty(r % kPfRing));
   };
+  // The same for a lone thread.
+  auto next_piece_lone = [&](int r) -> volatile int* {
+    const int k = r % kPfRing;
+    if (!mbar_wait(unit_full(k), (r / kPfRing) & 1, abort_flag)) return nullptr;
+    volatile int* const e = ring + 16 * k;
+    return e[kHead] >= 0 ? e : nullptr;
+  };
+  auto release_lone = [&](int r) { mbar_arrive(unit_empty(r % kPfRing)); };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -781,11 +789,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         bool ok = true;
 #pragma unroll 1
         for (int r = 0; ok; ++r) {
-          volatile int* const e = next_piece(r, ok);
+          volatile int* const e = next_piece_lone(r);
           if (e == nullptr) break;
           const PieceSteps steps = {e[kN0], e[kN1], e[kThin] != 0, it_base};
           it_base += 2 * e[kSteps];
-          release(r);
+          release_lone(r);
           op.nt = t ? steps.n1 : steps.n0;
           if (!mbar_wait(q_full(t), ui & 1, abort_flag)) break;
           if (op.nt == 0) mma_commit(q_empty(t));
@@ -840,10 +848,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
 
 #pragma unroll 1
       for (int k = 0; k < n; ++k, ++sj) {
-        if (!mbar_wait(s_full(t), sj & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), sj & 1, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         if (!idle) {
           uint32_t sv[128];
@@ -923,7 +929,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
 
       // ---- epilogue
       if (n > 0) {
-        if (!mbar_wait(o_full(t), ou & 1, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), ou & 1, abort_flag));
         ++ou;
       }
       tc_fence_after();
@@ -936,12 +942,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(merge_full);
-          if (!mbar_wait(merge_done, merges & 1, abort_flag)) ok = false;
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(merge_done, merges & 1, abort_flag));
           ++merges;
           tc_fence_after();
           continue;
         }
-        if (!mbar_wait(merge_full, merges & 1, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(merge_full, merges & 1, abort_flag));
         ++merges;
         tc_fence_after();
         const float2 o = merge_ml[r_in_tile];

@@ -1,5 +1,6 @@
 """Refusals of the paged cache's entry points on the host (no GPU), and the plain plan."""
 import ctypes
+import os
 
 import pytest
 
@@ -155,3 +156,12 @@ def test_plain_plan_by_hand():
     assert out[3] == [3, 4] + list(range(9)) + [7, -1, -1]
     assert out[4] == [23, 36] + [-1] * 9 + [35, -1, -1]
     assert out[5] == [2, 4]
+
+
+def test_warps_of_the_paged_kernels_meet_as_whole_warps():
+    """A piece's entries are given back by the warp that read them, all of its lanes: which lanes happen to be
+    active after a spin-wait says nothing about the others."""
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    for name in ("paged.cuh", "paged_decode.cuh", "paged_fwd.cuh", "page_plan.cuh", "piece_steps.h"):
+        with open(os.path.join(csrc, name)) as f:
+            assert "__activemask" not in f.read(), name
