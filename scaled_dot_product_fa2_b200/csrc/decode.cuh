@@ -106,9 +106,10 @@ __device__ __forceinline__ uint32_t sw128_off(int r, int c, int block_bytes) {
 // an empty batch still gets one slot (it writes o = 0, lse = -inf).  The
 // split kernel (slot -> batch) and the combine (batch -> slots) both derive
 // the deal from the lengths; every lane of the calling warp gets the same
-// answer.
-__device__ __forceinline__ int len_tiles(const int* __restrict__ seqlens, int bb, int B, int Sk) {
-  return bb < B ? (min(max(__ldg(seqlens + bb), 0), Sk) + kDecKeys - 1) / kDecKeys : 0;
+// answer.  (An ordinary load: the grid before may have written the lengths while
+// this one's CTAs were resident already.)
+__device__ __forceinline__ int len_tiles(const int* seqlens, int bb, int B, int Sk) {
+  return bb < B ? (min(max(seqlens[bb], 0), Sk) + kDecKeys - 1) / kDecKeys : 0;
 }
 
 // The deal holds the tile counts of up to kDealMaxBatch batches in registers
@@ -134,7 +135,7 @@ struct DealTiles {
   int t[kDealChunks];
 };
 
-__device__ __forceinline__ int slot_quota(const int* __restrict__ seqlens, int B, int Sk, int slots, int lane,
+__device__ __forceinline__ int slot_quota(const int* seqlens, int B, int Sk, int slots, int lane,
                                           DealTiles& dt) {
   int64_t tot = 0;
   int mx = 0;
@@ -180,7 +181,7 @@ struct SlotAssign {
 };
 
 // Requires use_deal(B, nsplit).
-__device__ __forceinline__ SlotAssign assign_slot(const int* __restrict__ seqlens, int B, int Sk, int slots, int j,
+__device__ __forceinline__ SlotAssign assign_slot(const int* seqlens, int B, int Sk, int slots, int j,
                                                   int lane) {
   DealTiles dt;
   const int q = slot_quota(seqlens, B, Sk, slots, lane, dt);
@@ -201,7 +202,7 @@ __device__ __forceinline__ SlotAssign assign_slot(const int* __restrict__ seqlen
 }
 
 // (first slot, slot count) of batch b.  Requires use_deal(B, nsplit).
-__device__ __forceinline__ int2 batch_slots(const int* __restrict__ seqlens, int B, int Sk, int slots, int b,
+__device__ __forceinline__ int2 batch_slots(const int* seqlens, int B, int Sk, int slots, int b,
                                             int lane) {
   DealTiles dt;
   const int q = slot_quota(seqlens, B, Sk, slots, lane, dt);
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(const __grid_
       k_in_batch = j - b * p.nsplit;
       quota = -1;
     }
-    const int raw = __ldg(p.seqlens_k + b);
+    const int raw = p.seqlens_k[b];
     L = min(max(raw, 0), p.Sk);
     if (raw != L && k_in_batch == 0 && rg == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(&g_error_word, kErrSeqlen);
     const int tiles = (L + kDecKeys - 1) / kDecKeys;

@@ -19,6 +19,10 @@ namespace sdpa {
 // head than this: a single token's, mostly.
 constexpr int kRowUnit = 16;
 
+// Lengths, offsets, tables and q may be what the grid before has just written, and these kernels start before
+// it ends (programmatic dependents): they are read with ordinary loads behind the dependency wait.  A
+// non-coherent load (ld.global.nc, __ldg) is for data that nobody writes while the kernel lives, and the compiler
+// may move it over the wait.
 struct PagedParams {
   const uint16_t* q;   // [T][Hq][d] bf16 (the decode: T = B * Sq)
   const uint16_t* k;   // element (page, head, row, c) at page*sp + head*sh + row*sr + c
@@ -58,7 +62,7 @@ struct PagedSeq {
 };
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
-  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), raw = __ldg(p.lens + b);
+  const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], raw = p.lens[b];
   PagedSeq s;
   s.start = min(max(c0, 0), p.T);
   const int end = min(max(c1, s.start), p.T);

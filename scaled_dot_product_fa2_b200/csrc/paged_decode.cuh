@@ -109,7 +109,7 @@ __device__ __forceinline__ PdSeq pd_seq(const PagedParams& p, int b) {
   PdSeq s;
   s.tok0 = b * p.Sq;
   s.cnt = p.Sq;
-  s.L = paged_clamp(p, __ldg(p.lens + b));
+  s.L = paged_clamp(p, p.lens[b]);
   s.lim = p.causal == 2 ? s.L - p.Sq : 0;
   s.T = pd_tiles(s.L);
   return s;
@@ -247,8 +247,8 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
     // last key).  It is looked at when the copy is issued, one tile later.
     auto has_copy = [&](int tl, int len) { return lane < 2 * nb && tl * kPdKeys + (box << pb_shift) < len; };
     auto page_of = [&](int bb, int tl, int len) -> int {
-      return has_copy(tl, len) ? __ldg(p.table + static_cast<int64_t>(bb) * p.max_pages +
-                                       ((tl * kPdKeys + (box << pb_shift)) >> p.page_shift))
+      return has_copy(tl, len) ? p.table[static_cast<int64_t>(bb) * p.max_pages +
+                                         ((tl * kPdKeys + (box << pb_shift)) >> p.page_shift)]
                                : 0;
     };
     int page = page_of(b, tile, s.L);
@@ -273,7 +273,7 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
                       (lane % kLines) * 64);
         }
       }
-      if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && __ldg(p.lens + b) != s.L)
+      if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && p.lens[b] != s.L)
         atomicOr(&g_error_word, kErrSeqlen);
       if (tile == 0 && n < s.T) {  // (never a small one)
         join = make_int4(s.tok0, hr, 0, s.cnt);
@@ -405,8 +405,8 @@ __device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const Pd
             p.q + (static_cast<int64_t>(tok0 + i) * p.Hq + head * p.group + g) * D);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          qf[ks][h] = live ? __ldg(q + ((ks * 16 + qc) >> 1)) : 0u;
-          qf[ks][2 + h] = live ? __ldg(q + ((ks * 16 + 8 + qc) >> 1)) : 0u;
+          qf[ks][h] = live ? q[(ks * 16 + qc) >> 1] : 0u;
+          qf[ks][2 + h] = live ? q[(ks * 16 + 8 + qc) >> 1] : 0u;
         }
       }
       for (int i = 0; i < n; ++i) {

@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
       auto has_copy = [&](int j, int L) { return copier && j * 128 + box * pb < L; };
       auto page_of = [&](int b, int j, int L) -> int {
         return has_copy(j, L)
-                   ? __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + ((j * 128 + box * pb) >> p.page_shift))
+                   ? p.table[static_cast<int64_t>(b) * p.max_pages + ((j * 128 + box * pb) >> p.page_shift)]
                    : 0;
       };
       int dealt = 0;  // whole units begun

@@ -78,6 +78,14 @@ __global__ void rope_lengths_kernel(const int* past_lens, int* total_lens, int B
   }
 }
 
+// A load of an input.  The paged form is a programmatic dependent: its entries, rows and tables may be what the
+// grid before has just written, and a non-coherent load is for data that nobody writes while the kernel lives.
+template <bool PAGED, class T>
+__device__ __forceinline__ T rope_load(const T* p) {
+  if constexpr (PAGED) return *p;
+  else return __ldg(p);
+}
+
 template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm : kRopeBlocksPerSm)
     rope_append_kernel(const __grid_constant__ RopeParams p) {
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
       const int h = h0 + u * kBlockRows + row_in_block;
-      x[u] = h < slots ? __ldg(src + h * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+      x[u] = h < slots ? rope_load<PAGED>(src + h * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   // Rotate and store the rows of one round.
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
   // whether it has a place or not: neither load waits for the other.
   auto entries = [&](int token) {
     if constexpr (PAGED) {
-      if (token < p.tokens) return make_int2(__ldg(p.slots + token), __ldg(p.positions + token));
+      if (token < p.tokens) return make_int2(p.slots[token], p.positions[token]);
     }
     return make_int2(-1, -1);
   };
@@ -223,7 +231,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
     if (pos >= 0) {
       const float4* cr = reinterpret_cast<const float4*>(p.cos_t + static_cast<int64_t>(pos) * kHalf + i0);
       const float4* sr = reinterpret_cast<const float4*>(p.sin_t + static_cast<int64_t>(pos) * kHalf + i0);
-      const float4 c0 = __ldg(cr), c1 = __ldg(cr + 1), s0 = __ldg(sr), s1 = __ldg(sr + 1);
+      const float4 c0 = rope_load<PAGED>(cr), c1 = rope_load<PAGED>(cr + 1);
+      const float4 s0 = rope_load<PAGED>(sr), s1 = rope_load<PAGED>(sr + 1);
       const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
       const float s[8] = {s0.x * sign, s0.y * sign, s0.z * sign, s0.w * sign,
                           s1.x * sign, s1.y * sign, s1.z * sign, s1.w * sign};

@@ -1,6 +1,7 @@
 """Refusals of the paged cache's entry points on the host (no GPU), and the plain plan."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -165,3 +166,17 @@ def test_warps_of_the_paged_kernels_meet_as_whole_warps():
     for name in ("paged.cuh", "paged_decode.cuh", "paged_fwd.cuh", "page_plan.cuh", "piece_steps.h"):
         with open(os.path.join(csrc, name)) as f:
             assert "__activemask" not in f.read(), name
+
+
+def test_programmatic_dependents_read_with_ordinary_loads():
+    """A kernel whose blocks are resident before the grid before it ends reads what that grid writes (lengths,
+    tables, slots, q) with ordinary loads: a non-coherent one may be answered from before the wait."""
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    for name in ("page_plan.cuh", "paged.cuh", "paged_decode.cuh", "paged_fwd.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            code = "\n".join(line.split("//")[0] for line in f.read().splitlines())
+        assert "__ldg" not in code and ".nc" not in code, name
+    with open(os.path.join(csrc, "decode.cuh")) as f:
+        assert not re.search(r"__ldg\((p\.)?seqlens", f.read())
+    with open(os.path.join(csrc, "rope.cuh")) as f:
+        assert not re.search(r"__ldg\((p\.(slots|positions)|src|cr|sr)", f.read())
