@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           op.nt = t ? steps.n1 : steps.n0;
           if (!mbar_wait(q_full(t), ui & 1, abort_flag)) break;
           if (op.nt == 0) mma_commit(q_empty(t));
-          ok = walk_piece(op, steps, t, seg);
+          ok = walk_piece<NS>(op, steps, t, seg);
           ++ui;
         }
         mma_commit(drain);
