@@ -436,8 +436,11 @@ attn_status_t attn_rope_append_paged(const void* packed_qkv, const float* cos_ta
  * [0, max_pages * page_size] or a cu_q that decreases or passes T is clamped
  * and reported (ATTN_ERR_SEQLEN); a page id outside [0, num_pages) reads as a
  * page of zeros and is reported (ATTN_ERR_PAGE).  What the pages hold behind a
- * sequence's last key has no effect, NaN included; a NaN or infinity among its
- * own keys or values may reach every row of that sequence.
+ * sequence's last key has no effect, NaN included.  A row that sees a score of
+ * NaN or +infinity (a NaN in its q or in a key, say) gets o = NaN and lse = NaN;
+ * one of -infinity has no weight, and rows that do not see such a key are what
+ * they are without it.  A NaN or infinity among a sequence's own values may
+ * reach every row of that sequence.
  *   workspace  attn_fwd_paged_workspace_size(...) bytes (about 45 MB, whatever
  *              the batch), device, 16-byte aligned, caller-owned; nothing in it
  *              needs to be initialised, and calls that may overlap on the GPU

@@ -84,6 +84,11 @@ __device__ __forceinline__ void paged_warm(const PagedParams& p) {
   }
 }
 
+// Whether a row (or a piece of its keys) with this running maximum and sum saw no key.  Only then is it left out:
+// a NaN score, or one of +infinity, makes the sum NaN (the maximum passes over a NaN), and that has to reach the
+// row's output and lse through every merge and join.
+__device__ __forceinline__ bool saw_nothing(float m, float l) { return m == -INFINITY && l == 0.f; }
+
 // a / b of non-negative values, by the 32-bit division where both fit.
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);

@@ -536,9 +536,9 @@ __device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const Pd
         const int r = qr + 8 * h;
         if (r < rows) {
           const float m1 = sm.s_m[mw * kPdRows + r], l1 = sm.s_l[mw * kPdRows + r];
-          const float M = fmaxf(l[h] > 0.f ? m[h] : -INFINITY, l1 > 0.f ? m1 : -INFINITY);
-          const float w0 = l[h] > 0.f ? ex2_approx((m[h] - M) * c) : 0.f;
-          const float w1 = l1 > 0.f ? ex2_approx((m1 - M) * c) : 0.f;
+          const float M = fmaxf(m[h], m1);  // (-inf where a warp saw nothing)
+          const float w0 = saw_nothing(m[h], l[h]) ? 0.f : ex2_approx((m[h] - M) * c);
+          const float w1 = saw_nothing(m1, l1) ? 0.f : ex2_approx((m1 - M) * c);
           m[h] = M;
           l[h] = l[h] * w0 + l1 * w1;
 #pragma unroll
@@ -573,12 +573,11 @@ __device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const Pd
       for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
       if (n > 0) {
 #pragma unroll
-        for (int w = 0; w < kPdWarps / 2; ++w)
-          if (sm.s_l[w * kPdRows + r] > 0.f) M = fmaxf(M, sm.s_m[w * kPdRows + r]);
+        for (int w = 0; w < kPdWarps / 2; ++w) M = fmaxf(M, sm.s_m[w * kPdRows + r]);
 #pragma unroll
         for (int w = 0; w < kPdWarps / 2; ++w) {
-          const float lw = sm.s_l[w * kPdRows + r];
-          wt[w] = lw > 0.f ? ex2_approx((sm.s_m[w * kPdRows + r] - M) * c) : 0.f;
+          const float lw = sm.s_l[w * kPdRows + r], mw = sm.s_m[w * kPdRows + r];
+          wt[w] = saw_nothing(mw, lw) ? 0.f : ex2_approx((mw - M) * c);
           sum += wt[w] * lw;
         }
 #pragma unroll
@@ -592,7 +591,8 @@ __device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const Pd
             acc[e + 3] += wt[w] * v.w;
           }
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const bool empty = saw_nothing(M, sum);
+      const float inv = empty ? 0.f : 1.f / sum;
       if (slot < 0) {
         const int i = row_token(p, row0 + r);
         const int hq = head * p.group + row0 + r - i * p.group;
@@ -603,14 +603,14 @@ __device__ __forceinline__ void pd_consumer(const PagedDecodeParams& a, const Pd
                                                           pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
         if (c0 == 0 && p.lse != nullptr)
           p.lse[a.lse_tok * tok0 + a.lse_head * hq + i] =
-              sum > 0.f ? M * p.scale + lg2_approx(sum) * 0.69314718055994531f : -INFINITY;
+              empty ? -INFINITY : M * p.scale + lg2_approx(sum) * 0.69314718055994531f;
       } else {
         float* const dst = a.part_o + (static_cast<int64_t>(slot) * kPdRows + r) * D + c0;
 #pragma unroll
         for (int e = 0; e < kCols; e += 4)
           *reinterpret_cast<float4*>(dst + e) =
               make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
-        if (c0 == 0) a.part_ml[slot * kPdRows + r] = make_float2(sum > 0.f ? M * p.scale : -INFINITY, sum);
+        if (c0 == 0) a.part_ml[slot * kPdRows + r] = make_float2(empty ? -INFINITY : M * p.scale, sum);
       }
     }
     named_bar_sync(bar, kPdWarps * 32);  // the merge buffer is read
@@ -748,22 +748,27 @@ __device__ __forceinline__ void paged_decode_join(const PagedDecodeParams& a, in
   if (row >= p.group * join.w) return;
   const int pieces = join.z - cta + 1;
   float M = -INFINITY;
+  bool some = false;  // whether any piece saw a key
   for (int s0 = 0; s0 < pieces; s0 += 32) {
     const float2 v = s0 == 0 ? ml : a.part_ml[slot_row(s0 + lane)];
-    if (s0 + lane < pieces && v.y > 0.f) M = fmaxf(M, v.x);
+    if (s0 + lane < pieces && !saw_nothing(v.x, v.y)) {
+      M = fmaxf(M, v.x);
+      some = true;
+    }
   }
+  some = __any_sync(0xffffffffu, some);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   float W = 0.f;
-  if (M != -INFINITY) {
+  if (some) {
     float w_lane = 0.f;
     for (int s0 = 0; s0 < pieces; s0 += kJoinRows) {
       if ((s0 & 31) == 0) {
         if (s0 > 0) ml = a.part_ml[slot_row(s0 + lane)];
-        w_lane = s0 + lane < pieces && ml.y > 0.f ? ml.y * ex2_approx((ml.x - M) * kLog2e) : 0.f;
+        w_lane = s0 + lane < pieces && !saw_nothing(ml.x, ml.y) ? ml.y * ex2_approx((ml.x - M) * kLog2e) : 0.f;
       }
       if (s0 > 0) {
 #pragma unroll
@@ -780,7 +785,7 @@ __device__ __forceinline__ void paged_decode_join(const PagedDecodeParams& a, in
       }
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = some ? 1.f / W : 0.f;
   const int i = row_token(p, row);
   const int hq = head * p.group + row - i * p.group;
   uint16_t* const dst = p.o + (static_cast<int64_t>(join.x + i) * p.Hq + hq) * D + lane * kPer;
@@ -789,7 +794,7 @@ __device__ __forceinline__ void paged_decode_join(const PagedDecodeParams& a, in
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
     p.lse[a.lse_tok * join.x + a.lse_head * hq + i] =
-        W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
+        some ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D>

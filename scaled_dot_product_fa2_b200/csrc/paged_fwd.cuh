@@ -951,15 +951,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
         ++merges;
         tc_fence_after();
         const float2 o = merge_ml[r_in_tile];
-        const float l1 = n_other > 0 && !idle ? o.y : 0.f;
+        const float l1 = n_other > 0 && !idle ? o.y : 0.f, m1 = n_other > 0 && !idle ? o.x : -INFINITY;
         have_other = n_other > 0;
-        const float M = fmaxf(l > 0.f ? m_used : -INFINITY, l1 > 0.f ? o.x : -INFINITY);
-        w0 = l > 0.f ? ex2_approx((m_used - M) * c) : 0.f;
-        w1 = l1 > 0.f ? ex2_approx((o.x - M) * c) : 0.f;
+        const float M = fmaxf(m_used, m1);
+        w0 = saw_nothing(m_used, l) ? 0.f : ex2_approx((m_used - M) * c);
+        w1 = saw_nothing(m1, l1) ? 0.f : ex2_approx((m1 - M) * c);
         m_used = M;
         l = l * w0 + l1 * w1;
       }
-      const bool empty_row = (m_used == -INFINITY) || !(l > 0.f);
+      const bool empty_row = saw_nothing(m_used, l);
       const float inv_l = empty_row ? 0.f : 1.f / l;
       const bool have_o = __all_sync(0xffffffffu, ok && n > 0);  // collective loads: warp-uniform
       have_other = __all_sync(0xffffffffu, ok && have_other);
@@ -1097,6 +1097,7 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
   // one pass with a running maximum, the loads of kAhead pieces at a time
   constexpr int kAhead = 3;
   float M = -INFINITY, W = 0.f;
+  bool some = false;  // whether any piece saw a key
   float acc[kPfJoinCols];
 #pragma unroll
   for (int i = 0; i < kPfJoinCols; ++i) acc[i] = 0.f;
@@ -1116,9 +1117,10 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (!(ml[u].y > 0.f)) continue;
+      if (saw_nothing(ml[u].x, ml[u].y)) continue;
+      some = true;
       const float m_new = fmaxf(M, ml[u].x);
-      const float down = M == -INFINITY ? 0.f : ex2_approx((M - m_new) * kLog2e);
+      const float down = saw_nothing(M, W) ? 0.f : ex2_approx((M - m_new) * kLog2e);
       const float w = ml[u].y * ex2_approx((ml[u].x - m_new) * kLog2e);
       M = m_new;
       W = W * down + w;
@@ -1126,7 +1128,7 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
       for (int i = 0; i < kPfJoinCols; ++i) acc[i] = fmaf(w, x[u][i], acc[i] * down);
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = some ? 1.f / W : 0.f;
   const int64_t token = j0.x + t * a.tpt + tok;
   uint16_t* const dst = p.o + (token * p.Hq + j0.y + head) * D + col;
 #pragma unroll
@@ -1136,7 +1138,7 @@ __device__ __forceinline__ void paged_fwd_join(const PagedFwdParams& a, int cta,
                    pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
   if (col == 0 && p.lse != nullptr)
     p.lse[static_cast<int64_t>(j0.y + head) * p.T + token] =
-        W > 0.f ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
+        some ? M + lg2_approx(W) * 0.69314718055994531f : -INFINITY;
 }
 
 // Both lines' joins in one launch of two blocks per CTA of the forward, all of which fit on the device
