@@ -109,8 +109,9 @@ __device__ __forceinline__ PdSeq pd_seq(const PagedParams& p, int b) {
   PdSeq s;
   s.tok0 = b * p.Sq;
   s.cnt = p.Sq;
-  s.L = paged_clamp(p, p.lens[b]);
-  s.lim = p.causal == 2 ? s.L - p.Sq : 0;
+  const int L = paged_clamp(p, p.lens[b]);
+  s.lim = p.causal == 2 ? L - p.Sq : 0;
+  s.L = paged_visible(p.causal, p.Sq, L, s.lim);
   s.T = pd_tiles(s.L);
   return s;
 }
@@ -273,7 +274,7 @@ __device__ __forceinline__ void pd_producer(const PagedDecodeParams& a, const Pd
                       (lane % kLines) * 64);
         }
       }
-      if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && p.lens[b] != s.L)
+      if (p.cu_q == nullptr && tile == 0 && hr == 0 && lane == 0 && p.lens[b] != paged_clamp(p, p.lens[b]))
         atomicOr(&g_error_word, kErrSeqlen);
       if (tile == 0 && n < s.T) {  // (never a small one)
         join = make_int4(s.tok0, hr, 0, s.cnt);
