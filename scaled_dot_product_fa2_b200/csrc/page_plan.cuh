@@ -45,7 +45,7 @@ constexpr int kPlanTokens = 2;          // consecutive tokens per thread and pas
 constexpr int kPlanMaxBatch = 16384;    // 3 ints of shared memory per request
 constexpr int kPlanMaxCluster = 16;     // with more than kPlanSmallBatch requests 8, the portable size: their CTAs'
 constexpr int kPlanSmallBatch = 4096;   // tables may leave room for one CTA per SM only
-constexpr uint32_t kPlanCap = 1u << 30; // prefix sums saturate here (above every legal total)
+constexpr uint32_t kPlanCap = (1u << 30) + 1;  // prefix sums saturate here: above every legal total (T is at most 2^30)
 constexpr int kPlanNotGranted = INT_MIN;
 
 inline int plan_smem_bytes(int B) { return (3 * B + 1) * 4; }

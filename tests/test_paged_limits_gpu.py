@@ -8,6 +8,8 @@ from tests.paged_ref import BHSD, TL, Batch, check
 
 pytestmark = pytest.mark.gpu
 
+PAGE = 14
+
 
 @pytest.fixture(scope="module")
 def sdpa():
@@ -42,4 +44,26 @@ def test_top_left_decode_reports_lengths_out_of_range(sdpa):
         with pytest.raises(_lib.AttnError) as e:
             sdpa.check_device_error()
         assert e.value.status == 13
+    sdpa.check_device_error()
+
+
+def test_plan_of_the_largest_number_of_tokens(sdpa):
+    """T = 2^30, its limit: a request whose tokens end behind the buffers is refused there as anywhere."""
+    T, page = 1 << 30, 256
+    free_mem, _ = torch.cuda.mem_get_info()
+    if free_mem < 12 << 30:
+        pytest.skip("two buffers of 4 GB")
+    pages = T // page
+    table = torch.full((2, pages), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(pages + 3, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    cu, total, pos, slot, rng = sdpa.attn_page_plan(ints([0, 5]), ints([T, 300]), table, free, ints([0, pages + 3]),
+                                                    page, T)
+    with pytest.raises(_lib.AttnError) as e:
+        sdpa.check_device_error()
+    assert e.value.status == PAGE
+    assert cu.tolist() == [0, T, T] and total.tolist() == [T, 5] and rng.tolist() == [pages, pages + 3]
+    assert (table[1] == -1).all() and torch.equal(table[0], free[:pages])
+    at = torch.tensor([0, 255, 256, T // 2 + 77, T - 257, T - 1], device="cuda")
+    assert torch.equal(pos[at].long(), at)
+    assert torch.equal(slot[at].long(), free[at // page].long() * page + at % page)
     sdpa.check_device_error()
