@@ -87,8 +87,8 @@ def _pages(k_pages, v_pages, layout, index, table=0, max_pages=0):
         raise ValueError("k_pages and v_pages must be dense inside a page")
     if N < 2:
         stride = 0
-    elif other[0] != stride:
-        raise ValueError("k_pages and v_pages must have one page stride")
+    elif other[0] != stride or stride == 0:  # (0: all pages in one place, which a call would take for dense ones)
+        raise ValueError("k_pages and v_pages must have one page stride, and pages that do not overlap")
     if layout == LAYOUT_BHSD:
         Hkv, P = s1, s2
     elif layout == LAYOUT_BSHD:

@@ -4,8 +4,9 @@ import os
 import re
 
 import pytest
+import torch
 
-from scaled_dot_product_fa2_b200 import _lib, build
+from scaled_dot_product_fa2_b200 import _lib, build, paged
 from tests import paged_ref
 
 P = 1 << 20  # a fake, well-aligned device address: every call here fails before it is used
@@ -180,3 +181,15 @@ def test_programmatic_dependents_read_with_ordinary_loads():
         assert not re.search(r"__ldg\((p\.)?seqlens", f.read())
     with open(os.path.join(csrc, "rope.cuh")) as f:
         assert not re.search(r"__ldg\((p\.(slots|positions)|src|cr|sr)", f.read())
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_pools_whose_pages_overlap_are_refused(layout):
+    """One page's memory for all of them (a stride of 0) is no pool: the C call takes 0 for dense pages."""
+    one = torch.zeros((1, 2, 16, 64) if layout == 0 else (1, 16, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        paged._pages(one.expand(5, -1, -1, -1), one.expand(5, -1, -1, -1), layout, -1)
+    both = torch.zeros((5, 2, *one.shape[1:]), dtype=torch.bfloat16)
+    for k, v in ((one, one), (both[:, 0], both[:, 1]), (both[:1, 0], both[:1, 1]), (both[:, 0].clone(), both[:, 1].clone())):
+        packed, Hkv, d = paged._pages(k, v, layout, -1)
+        assert (Hkv, d) == (2, 64)
