@@ -761,25 +761,25 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) paged_fwd_kernel(const __g
           int nt, pj;
           __device__ __forceinline__ bool p_ready() { return mbar_wait(p_bar, pj & 1, abort_flag); }
           __device__ __forceinline__ bool turn_ready(int s) { return mbar_wait(turn_bar, s & 1, abort_flag); }
-          __device__ __forceinline__ bool tile_ready(int i) { return mbar_wait(full(i % NS), (i / NS) & 1, abort_flag); }
-          __device__ __forceinline__ void multiply(int k, int v, int kt) {
+          __device__ __forceinline__ bool tile_ready(int i, int slot) { return mbar_wait(full(slot), (i / NS) & 1, abort_flag); }
+          __device__ __forceinline__ void multiply(int k, int vs, int ks) {
             tc_fence_after();
             if (k >= 1 && k - 1 < nt) {
-              const uint64_t vd = v_desc(v % NS);
+              const uint64_t vd = v_desc(vs);
               issue_pv<D, 0>(tO, tS, vd, k > 1);
               issue_pv<D, 1>(tO, tS, vd, true);
               ++pj;
               if (k == nt) mma_commit(o_bar);
             }
             if (k < nt) {
-              issue_qk<D>(tS, dq, k_desc(kt % NS));
+              issue_qk<D>(tS, dq, k_desc(ks));
               mma_commit(s_bar);
               if (k == nt - 1) mma_commit(q_bar);
             }
           }
-          __device__ __forceinline__ void free_tile(int i, int times) {
-            mma_commit(empty(i % NS));
-            if (times > 1) mma_commit(empty(i % NS));
+          __device__ __forceinline__ void free_tile(int slot, int times) {
+            mma_commit(empty(slot));
+            if (times > 1) mma_commit(empty(slot));
           }
           __device__ __forceinline__ void hand_over() { mbar_arrive(other_turn); }
         };

@@ -31,9 +31,9 @@ struct PieceSteps {
 // Segments of one piece for issuer t; `seg` counts them over all pieces.  Operations:
 //   p_ready()                  wait for P_t of the key tile before
 //   turn_ready(seg)            wait until the other issuer handed over
-//   tile_ready(i)              wait for ring index i
-//   multiply(k, v, kt)         issue segment k's products: V at ring index v, K at kt (-1: none)
-//   free_tile(i, times)        when the products so far are done, ring index i is free (`times` arrivals)
+//   tile_ready(i, slot)        wait for ring index i, which is in `slot`
+//   multiply(k, vs, ks)        issue segment k's products with V in slot vs and K in slot ks (-1: none)
+//   free_tile(slot, times)     when the products so far are done, the slot is free (`times` arrivals)
 //   hand_over()                the other issuer's turn
 // The waits return false where they gave up, and so does this.
 template <int NS, class Ops>
@@ -50,15 +50,17 @@ SDPA_HOST_DEVICE bool walk_piece(Ops& op, const PieceSteps& s, int t, int& seg) 
     const int vb = v - NS - s.it_base, kb = kt - NS - s.it_base;
     const bool v_early = vb >= 0 && (!s.thin || ((vb >> 1) & 1) == t);
     const bool k_early = kb >= 0 && (!s.thin || ((kb >> 1) & 1) == t);
-    if (v_early && !op.tile_ready(v)) return false;
-    if (k_early && !op.tile_ready(kt)) return false;
+    // slots: once, not in each operation (a prompt of 16384 tokens 2186 -> 2136 us)
+    const int vs = v >= 0 ? v % NS : -1, ks = kt >= 0 ? kt % NS : -1;
+    if (v_early && !op.tile_ready(v, vs)) return false;
+    if (k_early && !op.tile_ready(kt, ks)) return false;
     if (k >= 1 && k - 1 < nt && !op.p_ready()) return false;
     if ((t == 1 || seg >= 1) && !op.turn_ready(t == 1 ? seg : seg - 1)) return false;
-    if (v >= 0 && !v_early && !op.tile_ready(v)) return false;
-    if (kt >= 0 && !k_early && !op.tile_ready(kt)) return false;
-    op.multiply(k, v, kt);
-    if (v >= 0) op.free_tile(v, times);
-    if (kt >= 0) op.free_tile(kt, times);
+    if (v >= 0 && !v_early && !op.tile_ready(v, vs)) return false;
+    if (kt >= 0 && !k_early && !op.tile_ready(kt, ks)) return false;
+    op.multiply(k, vs, ks);
+    if (v >= 0) op.free_tile(vs, times);
+    if (kt >= 0) op.free_tile(ks, times);
     op.hand_over();
   }
   return true;

@@ -20,13 +20,25 @@ CHECK = r"""
 
 struct Event { char what; int i, n; };  // P: p, T: takes turn i, W: waits for tile i, M: multiply, F: frees i (n arrivals), H: hands over
 
+template <int NS>
 struct Record {
   std::vector<Event>& e;
+  int in_slot[NS];  // ring index that the issuer last waited for there
+  bool wrong;
+  explicit Record(std::vector<Event>& events) : e(events), wrong(false) {
+    for (int& i : in_slot) i = -1;
+  }
+  int tile(int slot) { return slot < 0 ? -1 : in_slot[slot]; }
   bool p_ready() { e.push_back({'P', 0, 0}); return true; }
   bool turn_ready(int s) { e.push_back({'T', s, 0}); return true; }
-  bool tile_ready(int i) { e.push_back({'W', i, 0}); return true; }
-  void multiply(int, int v, int k) { e.push_back({'M', v, k}); }
-  void free_tile(int i, int n) { e.push_back({'F', i, n}); }
+  bool tile_ready(int i, int slot) {
+    wrong |= slot != i % NS;
+    in_slot[slot] = i;
+    e.push_back({'W', i, 0});
+    return true;
+  }
+  void multiply(int, int vs, int ks) { e.push_back({'M', tile(vs), tile(ks)}); }
+  void free_tile(int slot, int n) { e.push_back({'F', tile(slot), n}); }
   void hand_over() { e.push_back({'H', 0, 0}); }
 };
 
@@ -51,8 +63,8 @@ static int replay(int pieces, int kind) {
     s.n1 = thin ? steps / 2 : steps;
     it_base += 2 * steps;
     for (int t = 0; t < 2; ++t) {
-      Record op{e[t]};
-      if (!sdpa::walk_piece<NS>(op, s, t, seg[t])) return 1;
+      Record<NS> op(e[t]);
+      if (!sdpa::walk_piece<NS>(op, s, t, seg[t]) || op.wrong) return 1;
     }
   }
   if (seg[0] != seg[1]) return 2;
