@@ -220,6 +220,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
     const int nbt = bt + gridDim.x;
     int nb = 0, nt = 0, nrow = 0, npos = -1;
     uint4 xn[kRopeUnroll];
+    float4 c0, c1, s0, s1;
+    auto load_angles = [&]() {
+      const float4* cr = reinterpret_cast<const float4*>(p.cos_t + static_cast<int64_t>(pos) * kHalf + i0);
+      const float4* sr = reinterpret_cast<const float4*>(p.sin_t + static_cast<int64_t>(pos) * kHalf + i0);
+      c0 = rope_load<PAGED>(cr);
+      c1 = rope_load<PAGED>(cr + 1);
+      s0 = rope_load<PAGED>(sr);
+      s1 = rope_load<PAGED>(sr + 1);
+    };
+    // ordinary loads stay where they stand: before the next token's (8192 tokens 38.4 -> 36.3 us)
+    if constexpr (PAGED) {
+      if (pos >= 0) load_angles();
+    }
     if (nbt < p.tokens) {
       if constexpr (PAGED) load_rows(nbt, 0, xn);
       npos = token_pos(nbt, next, nb, nt, nrow);
@@ -229,10 +242,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
       next = entries(nbt + gridDim.x);
     }
     if (pos >= 0) {
-      const float4* cr = reinterpret_cast<const float4*>(p.cos_t + static_cast<int64_t>(pos) * kHalf + i0);
-      const float4* sr = reinterpret_cast<const float4*>(p.sin_t + static_cast<int64_t>(pos) * kHalf + i0);
-      const float4 c0 = rope_load<PAGED>(cr), c1 = rope_load<PAGED>(cr + 1);
-      const float4 s0 = rope_load<PAGED>(sr), s1 = rope_load<PAGED>(sr + 1);
+      if constexpr (!PAGED) load_angles();
       const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
       const float s[8] = {s0.x * sign, s0.y * sign, s0.z * sign, s0.w * sign,
                           s1.x * sign, s1.y * sign, s1.z * sign, s1.w * sign};
