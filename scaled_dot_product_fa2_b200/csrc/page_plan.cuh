@@ -15,7 +15,7 @@
 // thread-block cluster scans all requests for itself (no exchange through
 // global memory), the cluster meets once, and the tokens are then spread over
 // all of its threads.  Nothing that an output may alias is read after that
-// meeting, so lengths and free range can be advanced in place.  Measured: 3.1 us
+// meeting, so lengths and free range can be advanced in place.  Measured: 3.2 us
 // for one token each of 8 requests, 6.5 us for 40 K tokens of 512.
 #pragma once
 #include <climits>

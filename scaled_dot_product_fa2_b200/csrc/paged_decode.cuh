@@ -30,8 +30,9 @@
 //   * K/V copies are the first to leave the L2 (each is read once): what a
 //     call's start needs, the code above all, stays there.
 // Measured on B200 (d = 128, 32 / 8 heads, three caches in rotation): 8 sequences
-// of 8192 keys 48.1 us = 5.58 TB/s, 64 of 20 to 8192 keys 57.4 us = 5.76 TB/s (85
-// and 88 % of a copy's rate); one of 700 keys 8.8 us, which is the fixed cost of
+// of 8192 keys 47.9 us = 5.60 TB/s, 64 of 20 to 8192 keys 58 us = 5.69 TB/s (86
+// and 87 % of a copy's rate), one of 131072 keys 88.9 us (92 %), of 32768 31.1 (66 %);
+// one of 700 keys 8.5 us, which is the fixed cost of
 // every call: lengths, table entry and first copy one after the other, the merge
 // and the join.  One CTA of eight warps per SM took 136.9 us for the 64 sequences
 // (short items leave the SM idle while they are merged), shares without an item

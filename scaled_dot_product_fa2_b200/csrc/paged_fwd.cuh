@@ -2,9 +2,12 @@
 // cache, on tcgen05 (see paged.cuh for the formula).
 //
 // Long chunks are bound by the tensor cores and single tokens by the bytes of
-// their cache; both come in one batch, so one kernel serves both, built like
-// the forward of prefill.cuh (same roles, barriers and softmax; the comments
-// there hold here) with these differences:
+// their cache; both come in one batch, so one kernel serves both.  Warps 0-7
+// are the softmax and epilogue of two 128-row query tiles (a thread per row: scores from
+// TMEM, running maximum and sum in fp32, P back to TMEM as bf16, O rescaled only where the
+// maximum has grown by kRescaleThreshold), warps 8 and 10 the tiles' MMA issuers, warp 9
+// the K/V producer and scheduler, warp 11 the Q loader.  What differs from the
+// contiguous forward of prefill.cuh:
 //   * A query tile packs the query heads of one KV head: row r of 128 is token
 //     r / hc, head r mod hc of the hc <= 128 heads (all of the group where it
 //     fits).  K/V are loaded once for the whole group, and a chunk of n tokens
@@ -22,7 +25,7 @@
 //     place from the lengths on the device.  A unit that crosses shares leaves
 //     one fp32 partial per CTA (two per CTA at most), which a second kernel, a
 //     programmatic dependent, joins in share order.
-//   * Cuts cost: partials, a piece more per CTA and the join, 14 us in all.  Where
+//   * Cuts cost: partials, a piece more per CTA and the join, 14 us in all (d = 128).  Where
 //     whole units balance as well or nearly (up to kPfRounds units a CTA, dealt in
 //     the order of their weights there and back), they stay whole.
 //   * What a sequence leaves behind its full units is the decode's work where it
@@ -40,14 +43,17 @@
 //     zeros (a page index behind the map's end).  The last page's rows behind
 //     the last key hold anything, and 0 times infinity or NaN is NaN, so warp 11
 //     zeroes them in V's last tile before the MMAs may read it.
-// Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 1.90 ms = 1157
-// TFLOP/s at full clocks (the contiguous forward: 1.81), 129 tokens behind 32639
-// keys 88.9 us = 777 TFLOP/s, a 2000-token chunk with 40 single tokens 69.0 us,
-// five prompts of 3 to 150 tokens 11.7 us.  A key step of a pair takes 2.1 us for
+// Measured on B200 (d = 128, 32 / 8 heads): a 16384-token prompt 2.01 ms = 1095
+// TFLOP/s at full clocks (the contiguous forward: 1.83) and 2.2 in long runs under the
+// power cap, 129 tokens behind 32639 keys 93 to 103 us = 740 to 670 TFLOP/s, a
+// 2000-token chunk with 40 single tokens 72 to 74 us, five prompts of 3 to 150
+// tokens 12.1 us.  A key step of a pair takes 2.1 us for
 // 1.1 us of tensor work: the softmax chain of one row per thread bounds it, as in
 // prefill.cuh.  The weights: at full clocks a step of 128 keys takes 2.1 us in a
 // pair and 1.7 us in a thin unit (its ring of five slots covers one copy's latency
-// per two tiles), a unit 3.2 us besides (first S, last P.V, stores).
+// per two tiles), a unit 3.2 us besides (first S, last P.V, stores).  They are
+// d = 128's, and d = 64 uses them: there a pair's step takes 2.05 us, a thin unit's
+// 1.0 (eight slots), so thin units end early beside pairs.
 #pragma once
 #include "paged_decode.cuh"
 #include "piece_steps.h"
@@ -67,7 +73,10 @@ constexpr int kPfQWarp = 11;     // loads Q; cleans V's last tile
 // (d = 128): a prompt of 1300 tokens, 32 / 8 heads, 34.2 whole, 41.3 cut; 2000 tokens of 32 heads without sharing 54.0
 // and 67.1; 25 chunks of 185 to 555 tokens, 16 / 2 heads, 79.6 and 88.7; 1024 tokens (4600 behind a share) 29.4 and
 // 34.1; the other way round 256 tokens after 1000 (8300 behind) 33.2 and 24.1, 2000 tokens of 16 / 2 heads (9500
-// behind) 48.1 and 42.6.  To look costs 0.6 us where the answer is no.
+// behind) 48.1 and 42.6.  Whole is better up to 4650 places behind (900 tokens, 31.0 and 32.8), cut from 8100 on (3000
+// tokens, 16 / 2 heads, 66.9 and 64.0).  d = 64, half the bytes a partial, uses the same limit and is better off cut
+// from about 4300 on: 1300 tokens (3800 behind) 31.7 whole, 32.9 cut, 900 tokens (4650) 27.4 and 26.0, 700 (4400) 23.1
+// and 20.7, 3000 tokens, 16 / 2 heads (8100) 59.0 and 52.1.  To look costs 0.6 us where the answer is no.
 constexpr float kPfJoinCost = 7000.f;
 constexpr int kPfRounds = 16;      // units of a CTA, at most; with more of them a cut weighs little
 
