@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, PAGED ? kRopePagedBlocksPerSm
       s0 = rope_load<PAGED>(sr);
       s1 = rope_load<PAGED>(sr + 1);
     };
-    // ordinary loads stay where they stand: before the next token's (8192 tokens 38.4 -> 36.3 us)
+    // ordinary loads stay where they stand: the angles' before those of the next token's rows (8192 tokens
+    // 38.4 -> 36.3 us)
     if constexpr (PAGED) {
       if (pos >= 0) load_angles();
     }
